@@ -11,6 +11,9 @@ process can load, the first call raises.
 
 NVFP4 block modes: nvfp4_quantize / fwht_quantize take four_six=True (four over six) or if4=True
 (IF4: E2M1 or INT4 per block, flagged in scale bit 7; read back with fp4_dequantize(fmt=IF4)).
+
+Key/value cache in 4 bits: fp4_kv_alloc makes the paged arrays, fp4_kv_append quantises new tokens
+into them, fp4_kv_read brings tokens back, fp4_kv_attention attends over them.
 """
 from __future__ import annotations
 
@@ -30,13 +33,14 @@ RNE, STOCHASTIC = 0, 1
 OCP_FLOOR, NOSAT_CEIL = 0, 1
 ROWMAJOR, MMA_TILED = 0, 1
 (OP_MX_QUANTIZE, OP_NVFP4_QUANTIZE, OP_FWHT_QUANTIZE, OP_DEQUANTIZE, OP_BLOCK_GEMM, OP_FWHT_QUANTIZE_STORED,
- OP_BLOCK_GEMM_IF4) = range(7)
+ OP_BLOCK_GEMM_IF4, OP_KV_ATTENTION) = range(8)
 STATUS = {0: "FP4_OK", 1: "FP4_EINVAL", 2: "FP4_EUNSUPPORTED", 3: "FP4_ECUDA"}
 
 # Every symbol include/fp4mx.h declares.
 EXPORTS = ("mx_quantize", "nvfp4_quantize", "fwht_quantize", "swiglu_fwht_quantize", "fp4_dequantize", "fp4_block_gemm",
            "fp4_workspace_size", "fp4_gemm_status_word", "fp4_status_str", "fp4_last_error",
-           "nvfp4_quantize_noalloc", "fp4_to_e4m3", "fp4_block_gemm_e4m3", "fp4_set_gemm_wait_limit")
+           "nvfp4_quantize_noalloc", "fp4_to_e4m3", "fp4_block_gemm_e4m3", "fp4_set_gemm_wait_limit",
+           "fp4_kv_append", "fp4_kv_read", "fp4_kv_attention")
 
 
 class Fp4Error(RuntimeError):
@@ -77,7 +81,13 @@ def lib() -> ctypes.CDLL:
     L.fp4_last_error.restype = ctypes.c_char_p
     L.fp4_set_gemm_wait_limit.argtypes = [ULL]
     L.fp4_set_gemm_wait_limit.restype = ULL
-    for name in ("mx_quantize", "nvfp4_quantize", "fwht_quantize", "swiglu_fwht_quantize", "fp4_dequantize",
+    cache = [P, P, P, P, LG, I, I, I]  # kq, ks, vq, vs, num_pages, page_size, heads, head_dim
+    table = [P, LG, I, I]              # table, table_stride, max_pages, seqs
+    L.fp4_kv_append.argtypes = [P, P, I, LG, LG, LG, LG, LG, P, I, I, I, P, P, *cache, P]
+    L.fp4_kv_read.argtypes = [*cache, I, I, P, P, *table, P, P, LG, I, P, P, P]
+    L.fp4_kv_attention.argtypes = [P, I, LG, LG, LG, I, *cache, I, I, P, P, *table, P, I, P, ctypes.c_float, I, I,
+                                   P, P, P, SZ, P]
+    for name in ("fp4_kv_append", "fp4_kv_read", "fp4_kv_attention", "mx_quantize", "nvfp4_quantize", "fwht_quantize", "swiglu_fwht_quantize", "fp4_dequantize",
                  "fp4_block_gemm", "fp4_to_e4m3", "fp4_block_gemm_e4m3"):
         getattr(L, name).restype = I
     _lib = L
@@ -322,3 +332,149 @@ def fp4_block_gemm_e4m3(A8: torch.Tensor, As: torch.Tensor, B8: torch.Tensor, Bs
     _check(lib().fp4_block_gemm_e4m3(M, N, K, _ptr(A8), _ptr(As), _ptr(B8), _ptr(Bs), _ptr(C), C.stride(0),
                                      _ptr(ws), ws.numel(), _stream(stream)))
     return C, ws
+
+
+# -------------------------------------------------------------------------------------------------
+# The paged 4-bit key/value cache.
+
+def fp4_kv_alloc(num_pages: int, heads: int, page_size: int, head_dim: int, fmt: int = NVFP4, device="cuda"):
+    """An empty paged cache: (kq, ks, vq, vs), uint8 [num_pages, heads, page_size, head_dim / 2] nibbles
+    and [num_pages, heads, page_size, head_dim / block] scale bytes of the keys and of the values."""
+    shape = (num_pages, heads, page_size)
+    half, nb = head_dim // 2, head_dim // (16 if fmt == NVFP4 else 32)
+    return tuple(torch.zeros(shape + (n,), dtype=torch.uint8, device=device) for n in (half, nb, half, nb))
+
+
+def _kv_same_device(device, **ts):
+    for name, t in ts.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} is on {t.device}, not on {device}")
+
+
+def _kv_ints(name, t, dtype, *shape):
+    """A contiguous integer tensor of the given shape (None: any extent)."""
+    if t is None:
+        return
+    if t.dtype != dtype or t.dim() != len(shape) or any(n is not None and m != n for m, n in zip(t.shape, shape)) \
+            or not t.is_contiguous():
+        want = ", ".join("any" if n is None else str(n) for n in shape)
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor [{want}], got {t.dtype} {list(t.shape)}")
+
+
+def _kv_cache(cache, fmt, k_global, v_global):
+    """The cache's part of the argument lists: (arrays and sizes, format and scales), and its device."""
+    kq, ks, vq, vs = cache
+    if kq.dim() != 4 or not kq.is_cuda:
+        raise ValueError("the cache's arrays are CUDA tensors [pages, heads, page, bytes]")
+    pages, heads, page, half = kq.shape
+    block = 32 if fmt == MXFP4 else 16
+    for name, t, n in (("kq", kq, half), ("ks", ks, 2 * half // block), ("vq", vq, half), ("vs", vs, 2 * half // block)):
+        if t.dtype != torch.uint8 or tuple(t.shape) != (pages, heads, page, n) or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous uint8 tensor {[pages, heads, page, n]}, got {t.dtype} {list(t.shape)}")
+    for name, t in (("k_global", k_global), ("v_global", v_global)):
+        if t is not None and (t.dtype != torch.float32 or t.numel() != 1):
+            raise ValueError(f"{name} must be a float32 tensor of one element")
+    _kv_same_device(kq.device, ks=ks, vq=vq, vs=vs, k_global=k_global, v_global=v_global)
+    return ([_ptr(kq), _ptr(ks), _ptr(vq), _ptr(vs), pages, page, heads, 2 * half],
+            [fmt, block, _ptr(k_global), _ptr(v_global)], kq.device)
+
+
+def _kv_table(table, seqs):
+    if table.dtype != torch.int32 or table.dim() != 2 or table.shape[0] != seqs or (table.numel() and table.stride(1) != 1):
+        raise ValueError(f"block table: expected int32 [{seqs}, pages] with adjacent entries, got {table.dtype} {list(table.shape)}")
+    return [_ptr(table), table.stride(0), table.shape[1], seqs]
+
+
+def _kv_strides(t):
+    """Token and head strides of [tokens, heads, head_dim]; an extent of one has none that matters."""
+    return [0 if t.shape[i] <= 1 else t.stride(i) for i in (0, 1)]
+
+
+def _kv_stream(device, stream):
+    """The stream of the call (torch's current one on `device` by default)."""
+    return torch.cuda.current_stream(device) if stream is None else stream
+
+
+def fp4_kv_append(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, fmt: int = NVFP4,
+                  four_six: bool = False, k_global: torch.Tensor | None = None, v_global: torch.Tensor | None = None,
+                  stream=None) -> None:
+    """Quantise the keys and values of new tokens into the paged cache (from fp4_kv_alloc).
+    k, v: bf16 or fp32 [tokens, heads, head_dim], any token and head strides (slices of a fused
+    projection); slots: int64 [tokens], page * page_size + offset, negative to skip a row; k_global,
+    v_global: the fixed NVFP4 scales, amax / (6 * 448), or amax / (6 * 256) with four_six."""
+    arrays, form, device = _kv_cache(cache, fmt, k_global, v_global)
+    heads, dim = arrays[6], arrays[7]
+    if k.dim() != 3 or v.shape != k.shape or v.dtype != k.dtype or tuple(k.shape[1:]) != (heads, dim):
+        raise ValueError(f"k and v: expected [tokens, {heads}, {dim}] of one dtype, got {list(k.shape)} and {list(v.shape)}")
+    if k.numel() and (k.stride(2) != 1 or v.stride(2) != 1):
+        raise ValueError("the channels of k and v must be adjacent")
+    _kv_ints("slots", slots, torch.int64, k.shape[0])
+    _kv_same_device(device, k=k, v=v, slots=slots)
+    with torch.cuda.device(device):
+        _check(lib().fp4_kv_append(_ptr(k), _ptr(v), _dtype_code(k), k.shape[0], *_kv_strides(k), *_kv_strides(v), _ptr(slots), form[0], form[1], _nv_mode(four_six, False), *form[2:],
+                                   *arrays, _stream(_kv_stream(device, stream))))
+
+
+def fp4_kv_read(cache, table: torch.Tensor, cu: torch.Tensor, total: int, fmt: int = NVFP4,
+                starts: torch.Tensor | None = None, out_dtype: torch.dtype = torch.bfloat16,
+                k_global: torch.Tensor | None = None, v_global: torch.Tensor | None = None, out=None, stream=None):
+    """Dequantise ranges of the cache: rows cu[b]..cu[b+1]-1 of the outputs are tokens starts[b].. (0..
+    without `starts`) of sequence b.  cu: int32 [seqs + 1]; total: rows of the outputs, cu[-1] for
+    the caller that knows it.  Returns (k, v) [total, heads, head_dim] in out_dtype, or fills
+    `out` = (k, v) (rows from cu[-1] on are left as they were)."""
+    arrays, form, device = _kv_cache(cache, fmt, k_global, v_global)
+    seqs = cu.numel() - 1
+    _kv_ints("cu", cu, torch.int32, None)
+    _kv_ints("starts", starts, torch.int32, seqs)
+    where = _kv_table(table, seqs)
+    _kv_same_device(device, table=table, cu=cu, starts=starts)
+    s = _kv_stream(device, stream)
+    shape = (total, arrays[6], arrays[7])
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        if out is None:
+            out = tuple(torch.empty(shape, dtype=out_dtype, device=device) for _ in range(2))
+        k, v = out
+        for t in out:
+            if tuple(t.shape) != shape or t.dtype != k.dtype or t.device != device or not t.is_contiguous():
+                raise ValueError(f"out: expected two contiguous tensors {list(shape)} of one dtype on {device}")
+        _check(lib().fp4_kv_read(*arrays, *form, *where, _ptr(cu), _ptr(starts), total, _dtype_code(k), _ptr(k), _ptr(v),
+                                 _stream(s)))
+    return k, v
+
+
+def fp4_kv_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor, fmt: int = NVFP4,
+                     cu_q: torch.Tensor | None = None, max_q: int = 1, scale: float | None = None,
+                     causal: bool = True, window: int = 0, want_lse: bool = False,
+                     k_global: torch.Tensor | None = None, v_global: torch.Tensor | None = None,
+                     out: torch.Tensor | None = None, stream=None, workspace: torch.Tensor | None = None):
+    """Attention of bf16 queries q [total_q, q_heads, head_dim] (any token and head strides) over the
+    cache.  Query head h reads key/value head h // (q_heads // heads); the queries of a sequence are
+    its last tokens.  lens: int32 [seqs], keys of each sequence; cu_q: int32 [seqs + 1], queries
+    cu_q[b]..cu_q[b+1]-1 belong to sequence b, at most max_q each (without it, max_q for every
+    sequence); scale: 1 / sqrt(head_dim) by default; window: keys a query sees, itself the last one (0:
+    all).  Returns (out bf16 [total_q, q_heads, head_dim], lse float32 [total_q, q_heads] or None);
+    a query that sees no key gives zeros and lse = -inf."""
+    arrays, form, device = _kv_cache(cache, fmt, k_global, v_global)
+    if q.dim() != 3 or q.shape[2] != arrays[7]:
+        raise ValueError(f"q: expected [tokens, query heads, {arrays[7]}], got {list(q.shape)}")
+    if q.numel() and q.stride(2) != 1:
+        raise ValueError("the channels of q must be adjacent")
+    total, q_heads, dim = q.shape
+    seqs = lens.numel()
+    _kv_ints("lens", lens, torch.int32, None)
+    _kv_ints("cu_q", cu_q, torch.int32, seqs + 1)
+    where = _kv_table(table, seqs)
+    _kv_same_device(device, q=q, table=table, lens=lens, cu_q=cu_q, out=out, workspace=workspace)
+    s = _kv_stream(device, stream)
+    with torch.cuda.device(device), torch.cuda.stream(s):
+        if out is None:
+            out = torch.empty((total, q_heads, dim), dtype=torch.bfloat16, device=device)
+        elif tuple(out.shape) != (total, q_heads, dim) or out.dtype != torch.bfloat16 or not out.is_contiguous():
+            raise ValueError(f"out: expected a contiguous bfloat16 tensor {[total, q_heads, dim]}")
+        lse = torch.empty((total, q_heads), dtype=torch.float32, device=device) if want_lse else None
+        ws = workspace if workspace is not None else _workspace(OP_KV_ATTENTION, device, total, q_heads)
+        _check(lib().fp4_kv_attention(_ptr(q), _dtype_code(q), total, *_kv_strides(q), q_heads, *arrays, *form,
+                                      *where, _ptr(cu_q), max_q, _ptr(lens),
+                                      dim ** -0.5 if scale is None else float(scale), int(causal), window, _ptr(out),
+                                      _ptr(lse), _ptr(ws), ws.numel() * ws.element_size(), _stream(s)))
+    return out, lse

@@ -108,6 +108,7 @@ size_t fp4_workspace_size(fp4_op op, long rows, long cols) {
     case FP4_OP_BLOCK_GEMM_IF4:
       // rows = M + N, cols = K: the status word, padding, and both fp16 operands
       return rows > 0 && cols > 0 ? 2 * kGemmWorkspace + 2 * (size_t)rows * (size_t)cols : kGemmWorkspace;
+    case FP4_OP_KV_ATTENTION: return fp4k::kv_attention_workspace();
     default: return 0;
   }
 }

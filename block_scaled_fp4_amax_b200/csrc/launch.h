@@ -96,6 +96,63 @@ struct GemmLaunch {
   uint32_t* status;  // device status word
 };
 
+// The paged 4-bit key/value cache: nibbles [num_pages, heads, page, head_dim / 2] and scale bytes
+// [num_pages, heads, page, head_dim / block] for the keys and for the values.
+struct KvCache {
+  uint8_t *kq, *ks, *vq, *vs;
+  long long num_pages;
+  int page_shift;  // log2 of the page size
+  int heads, head_dim;
+  bool nv;         // NVFP4 (block 16, E4M3) or MXFP4 (block 32, E8M0)
+  const float *k_global, *v_global;  // NVFP4
+};
+
+struct KvAppendLaunch {
+  KvCache c;
+  const void *k, *v;
+  bool bf16;
+  long long tokens;
+  long long k_stride, k_head_stride, v_stride, v_head_stride;  // elements
+  const long long* slots;
+  int mode;        // NVFP4 block mode: 0 plain, 1 four-over-six
+};
+
+struct KvReadLaunch {
+  KvCache c;
+  const int* table;
+  long long table_stride;
+  int max_pages, seqs;
+  const int *starts, *cu;
+  long long total;
+  bool out_bf16;
+  void *k_out, *v_out;
+};
+
+struct KvAttentionLaunch {
+  KvCache c;
+  const void* q;   // bf16
+  long long q_stride, q_head_stride;  // elements
+  long long total_q;
+  int q_heads;
+  const int* table;
+  long long table_stride;
+  int max_pages, seqs;
+  const int* cu_q;  // nullptr: max_q queries for every sequence
+  int max_q;
+  const int* lens;
+  float scale;
+  int causal, window;
+  void* out;       // bf16 [total_q, q_heads, head_dim]
+  float* lse;      // [total_q, q_heads] or nullptr
+  void* workspace;
+};
+
+cudaError_t launch_kv_append(const KvAppendLaunch& L, cudaStream_t s);
+cudaError_t launch_kv_read(const KvReadLaunch& L, cudaStream_t s);
+cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t s);
+// Bytes of workspace launch_kv_attention needs on the current device.
+size_t kv_attention_workspace();
+
 cudaError_t launch_quantize(const QuantLaunch& L, cudaStream_t s);
 // Upper bound of the tensor-amax pass's grid: the number of 32-bit slots its output needs.
 constexpr int kAmaxSlots = 2048;

@@ -30,19 +30,6 @@ constexpr int kUnroll46 = 2;    // four-over-six and IF4: compute-bound, so a sm
 constexpr int kPlain = 0, kFourSix = 1, kIF4 = 2;
 
 // ---------------------------------------------------------------------------------------------
-// MXFP4 shared exponent from the amax bit pattern (exact): OCP floor(log2 amax) - 2, or the
-// smallest e with amax <= 6 * 2^e; clamped to [-127, 127]; an all-zero block takes e = 0.  A
-// non-finite maximum (Inf or NaN: exponent field 255) counts as 2^128, e = 126 under both rules.
-__device__ __forceinline__ int mx_exponent(uint32_t bits, int policy) {
-  const int ef = (int)((bits >> 23) & 0xFFu);
-  if (bits == 0u) return 0;
-  if (ef == 0) return -127;  // subnormal maximum: below 2^-126, clamps
-  if (ef == 255) return 126;
-  const int E = ef - 127;
-  const int e = (policy == 0) ? E - 2 : (((bits & 0x7FFFFFu) <= 0x400000u) ? E - 2 : E - 1);
-  return e < -127 ? -127 : e;
-}
-
 struct NvScale {
   float s_g, inv6, inv4;
 };

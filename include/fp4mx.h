@@ -113,7 +113,7 @@ typedef struct fp4_counts {
  * fp32 rotation of a [rows, cols] tensor, which lets the two-pass NVFP4 call rotate once. */
 typedef enum fp4_op { FP4_OP_MX_QUANTIZE = 0, FP4_OP_NVFP4_QUANTIZE = 1, FP4_OP_FWHT_QUANTIZE = 2,
                       FP4_OP_DEQUANTIZE = 3, FP4_OP_BLOCK_GEMM = 4, FP4_OP_FWHT_QUANTIZE_STORED = 5,
-                      FP4_OP_BLOCK_GEMM_IF4 = 6 } fp4_op;
+                      FP4_OP_BLOCK_GEMM_IF4 = 6, FP4_OP_KV_ATTENTION = 7 } fp4_op;
 
 /* ---------------------------------------------------------------------------------------------
  * mx_quantize — MXFP4 quantisation of a row-major [rows, cols] tensor, blocks of 32 along rows.
@@ -311,6 +311,94 @@ FP4_API fp4_status nvfp4_quantize_noalloc(const void* x, fp4_dtype dtype, long r
                                           fp4_scale_layout layout, const float* global_in, float* global_out,
                                           unsigned char* q, unsigned char* scales, fp4_counts* counts,
                                           void* stream);
+
+/* ---------------------------------------------------------------------------------------------
+ * The paged 4-bit key/value cache of an attention layer: three calls that write it, read it back and
+ * attend over it.  The source pages quantise weights and activations ([E] §2); the cache keeps the
+ * same two formats for keys and values.
+ *
+ * Layout.  A page holds page_size consecutive tokens of one sequence for every key/value head:
+ *   kq, vq : device [num_pages, heads, page_size, head_dim / 2] packed E2M1 (element 2j in the low
+ *            nibble of byte j), 16-byte aligned;
+ *   ks, vs : device [num_pages, heads, page_size, head_dim / B] scale bytes (E4M3, B = 16, under
+ *            FP4_NVFP4; E8M0, B = 32, under FP4_MXFP4), 16-byte aligned.
+ * One token of one head is one row of head_dim values; its bytes are those nvfp4_quantize (with
+ * global_in) or mx_quantize (FP4_MX_OCP_FLOOR) writes for that row, except that an MXFP4 cache
+ * keeps its exponents within -23 .. 13 (bytes 104 .. 140), so that every value it holds is exactly
+ * an fp16 number, which the attention kernels multiply in: magnitudes above 6 * 2^13 saturate, and
+ * blocks below 2^-21 are rounded to multiples of 2^-24.  FP4_IF4 is FP4_EUNSUPPORTED.
+ * Preconditions of all three: head_dim 64 or 128, page_size a power of two in 16 .. 1024, 1 <= heads
+ * <= 1024, 1 <= num_pages < 2^31, B == the format's block size.
+ *   k_global, v_global : device floats, the per-tensor scales s_g of keys and values (FP4_NVFP4;
+ *            ignored for FP4_MXFP4).  A cache is written token by token, so the caller fixes them.
+ * Block table: int32 [seqs, max_pages] on the device with `table_stride` (elements) between
+ * sequences; entry p of a row is the page holding tokens p * page_size and up.  An entry outside
+ * [0, num_pages) is no page: its tokens read as zeros and attention does not see them.
+ * --------------------------------------------------------------------------------------------- */
+
+/* fp4_kv_append — quantise the keys and values of `tokens` new tokens into the cache.
+ *   k, v   : device [tokens, heads, head_dim] of `dtype`; element (t, h, i) at t * stride + h *
+ *            head_stride + i.  32-byte aligned, strides multiples of 32 bytes (slices of a fused
+ *            projection qualify).
+ *   slots  : device int64 [tokens]: page * page_size + offset.  A slot outside the cache (negative,
+ *            for a padded row) writes nothing.  Slots of one call must differ: a slot named twice
+ *            holds a mix of the two tokens' bytes.
+ *   mode   : FP4_NV_PLAIN, or FP4_NV_FOUR_SIX (FP4_NVFP4 only).  Round to nearest.
+ * A block holding Inf or NaN is left unspecified, as by the quantisers. */
+FP4_API fp4_status fp4_kv_append(const void* k, const void* v, fp4_dtype dtype, long tokens, long k_stride,
+                                 long k_head_stride, long v_stride, long v_head_stride, const long long* slots,
+                                 fp4_format format, int block, int mode, const float* k_global,
+                                 const float* v_global, unsigned char* kq, unsigned char* ks, unsigned char* vq,
+                                 unsigned char* vs, long num_pages, int page_size, int heads, int head_dim,
+                                 void* stream);
+
+/* fp4_kv_read — dequantise ranges of the cache back into dense rows.
+ *   cu     : device int32 [seqs + 1], ascending from 0: output rows cu[b] .. cu[b + 1] - 1 are tokens
+ *            starts[b], starts[b] + 1, ... of sequence b.
+ *   starts : device int32 [seqs], or NULL (0 for every sequence).
+ *   total  : rows of the outputs; rows from cu[seqs] on are left as they were.
+ *   k_out, v_out : device [total, heads, head_dim] of out_dtype, 32-byte aligned; values as
+ *            fp4_dequantize gives them.  Tokens without a page (before 0 or beyond the table too)
+ *            read as zeros. */
+FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks, const unsigned char* vq,
+                               const unsigned char* vs, long num_pages, int page_size, int heads, int head_dim,
+                               fp4_format format, int block, const float* k_global, const float* v_global,
+                               const int* table, long table_stride, int max_pages, int seqs, const int* cu,
+                               const int* starts, long total, fp4_dtype out_dtype, void* k_out, void* v_out,
+                               void* stream);
+
+/* fp4_kv_attention — softmax(scale * q K^T + mask) V over the cache, for one query token a sequence
+ * (decoding), a few (verification of drafted tokens) or many (prompts, whole or in chunks).
+ * Query head h reads key/value head h / (q_heads / heads).  The queries of a sequence are its last
+ * tokens: query i of n sits at position lens[b] - n + i, and sees key j
+ *   iff j < lens[b], and j <= its position (causal != 0), and j > its position - window (window > 0),
+ *   and the key has a page.  A query that sees no key gives zeros and lse = -inf.
+ * Scores, softmax statistics and sums are fp32; keys and values enter the products exactly, the
+ * queries too (scaled per row by a power of two), and the softmax weights, fp32 in the sum that
+ * divides, are rounded to fp16 (2^-12 of each weight) for the product with V.  A query row holding
+ * Inf or NaN, and an MXFP4 scale byte outside 104 .. 140, leave the rows that meet them unspecified;
+ * an E4M3 NaN scale byte of a key gives NaN in the rows that see it, one of a value block counts as 0
+ * (a product with a weight of 0 would carry it into rows that do not see the token).
+ *   q     : device bf16 [total_q, q_heads, head_dim]; strides (elements) as in fp4_kv_append;
+ *           16-byte aligned, strides multiples of 16 bytes.  dtype must be FP4_BF16.
+ *   cu_q  : device int32 [seqs + 1], ascending from 0: queries cu_q[b] .. cu_q[b + 1] - 1 belong to
+ *           sequence b; NULL: max_q for every sequence (total_q == seqs * max_q).  Rows from
+ *           cu_q[seqs] on are left as they were.
+ *   max_q : at least the largest number of queries of a sequence; further ones are not computed.
+ *   lens  : device int32 [seqs]: keys of each sequence, the new tokens' included (append first);
+ *           negative counts as 0, more than max_pages * page_size as that.
+ *   out   : device bf16 [total_q, q_heads, head_dim], 16-byte aligned.
+ *   lse   : device float [total_q, q_heads] or NULL: natural log of the sum of exp(scale q k).
+ *   workspace : device, 16-byte aligned, >= fp4_workspace_size(FP4_OP_KV_ATTENTION, total_q, q_heads)
+ *           bytes; clobbered, needs no initialisation.  Calls that overlap need one each. */
+FP4_API fp4_status fp4_kv_attention(const void* q, fp4_dtype dtype, long total_q, long q_stride,
+                                    long q_head_stride, int q_heads, const unsigned char* kq,
+                                    const unsigned char* ks, const unsigned char* vq, const unsigned char* vs,
+                                    long num_pages, int page_size, int heads, int head_dim, fp4_format format,
+                                    int block, const float* k_global, const float* v_global, const int* table,
+                                    long table_stride, int max_pages, int seqs, const int* cu_q, int max_q,
+                                    const int* lens, float scale, int causal, int window, void* out, float* lse,
+                                    void* workspace, size_t ws_bytes, void* stream);
 
 /* Bytes of device workspace `op` needs for the given sizes (rows/cols; M/N for the GEMM). */
 FP4_API size_t fp4_workspace_size(fp4_op op, long rows, long cols);

@@ -1,0 +1,406 @@
+"""GPU tests of the paged 4-bit key/value cache: bytes against the oracle, reads against its
+dequantiser, attention against the formula in 64 bits (tests/kv.py derives the bounds)."""
+import numpy as np
+import pytest
+import torch
+
+import block_scaled_fp4_amax_b200 as fp4
+import oracle as O
+from kv import FORMATS, Cache, attention64, block_of, check, quantise, run_and_check
+
+pytestmark = pytest.mark.gpu
+
+SENTINEL = 0xA5
+
+
+def sentinel_cache(pages, heads, page, dim, fmt, device):
+    return tuple(t.fill_(SENTINEL) for t in fp4.fp4_kv_alloc(pages, heads, page, dim, fmt, device=device))
+
+
+def scales_for(fmt, device, k=0.0021, v=0.0016):
+    if fmt == fp4.MXFP4:
+        return {}
+    return {n: torch.tensor([g], dtype=torch.float32, device=device) for n, g in (("k_global", k), ("v_global", v))}
+
+
+# ---------------------------------------------------------------------------------------------
+# append
+
+@pytest.mark.parametrize("fmt,four_six", [("nvfp4", False), ("nvfp4", True), ("mxfp4", False)])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("tokens,heads,dim,page,layout", [
+    (1, 8, 128, 16, "dense"), (1, 1, 64, 16, "fused"), (37, 3, 64, 32, "fused"), (50, 2, 128, 64, "head_major"),
+    (129, 5, 128, 128, "dense"), (7, 1, 128, 1024, "dense")])
+def test_append_bytes(cuda, fmt, four_six, dtype, tokens, heads, dim, page, layout):
+    rng = np.random.default_rng(tokens + dim)
+    f = FORMATS[fmt]
+    pages = -(-tokens // page) + 3
+    cache = sentinel_cache(pages, heads, page, dim, f, cuda)
+    # outlier channels, exact zeros and lattice points (ties, equal four-over-six errors)
+    x = rng.standard_normal((2, tokens, heads, dim)) * (1 + 30 * (rng.random(dim) < 0.02))
+    x[:, ::3] = rng.integers(-48, 49, size=x[:, ::3].shape) / 8
+    x[:, :, :, 3] = 0
+    wide = torch.from_numpy(x.astype(np.float32)).to(dtype)
+    if layout == "fused":
+        both = torch.zeros(tokens, 4 * heads, dim, dtype=dtype)
+        both[:, heads:2 * heads], both[:, 3 * heads:] = wide[0], wide[1]
+        both = both.to(cuda)
+        k, v = both[:, heads:2 * heads], both[:, 3 * heads:]
+    elif layout == "head_major":
+        k, v = (w.transpose(0, 1).contiguous().to(cuda).transpose(0, 1) for w in wide)
+    else:
+        k, v = wide[0].to(cuda), wide[1].to(cuda)
+    slots = rng.permutation(pages * page)[:tokens].astype(np.int64)
+    slots[1::5] = -1 - slots[1::5]          # skipped rows
+    if tokens > 8:
+        slots[6] = pages * page             # one past the end: skipped too
+    sc = scales_for(f, cuda)
+    fp4.fp4_kv_append(k, v, cache, torch.from_numpy(slots).to(cuda), f, four_six=four_six, **sc)
+    torch.cuda.synchronize()
+    for which, g in ((0, 0.0021), (1, 0.0016)):
+        want_q = np.full((pages, heads, page, dim // 2), SENTINEL, np.uint8)
+        want_s = np.full((pages, heads, page, dim // block_of(f)), SENTINEL, np.uint8)
+        q, s = quantise(wide[which].float().numpy(), f, g, four_six)
+        live = (slots >= 0) & (slots < pages * page)
+        want_q[slots[live] // page, :, slots[live] % page] = q[live]
+        want_s[slots[live] // page, :, slots[live] % page] = s[live]
+        assert np.array_equal(cache[2 * which].cpu().numpy(), want_q)
+        assert np.array_equal(cache[2 * which + 1].cpu().numpy(), want_s)
+
+
+def test_append_mx_exponent_range(cuda):
+    """Block maxima beyond the cache's exponents: the exponent is clamped to -23..13, the codes are
+    those of that exponent."""
+    exps = [-140, -126, -40, -25, -24, -22, -21, -20, 0, 14, 15, 16, 17, 40, 120]
+    rng = np.random.default_rng(3)
+    x = np.zeros((len(exps), 1, 64), dtype=np.float32)
+    for i, e in enumerate(exps):
+        x[i, 0] = np.ldexp(rng.uniform(-1, 1, 64), e).astype(np.float32)
+    x[2, 0, 32:] = 0
+    t = torch.from_numpy(x).to(cuda)
+    cache = fp4.fp4_kv_alloc(1, 1, 16, 64, fp4.MXFP4, device=cuda)
+    fp4.fp4_kv_append(t, t, cache, torch.arange(len(exps), device=cuda), fp4.MXFP4)
+    q, s = cache[0].cpu().numpy()[0, 0], cache[1].cpu().numpy()[0, 0]
+    for i in range(len(exps)):
+        for blk in range(2):
+            xb = x[i, 0, 32 * blk:32 * blk + 32]
+            e = min(max(O.mx_exponent(float(np.abs(xb).max())), -23), 13)
+            codes = O.mx_encode_block(xb, e)[0]
+            assert s[i, blk] == e + 127
+            packed = np.asarray(codes[0::2]) | (np.asarray(codes[1::2]) << 4)
+            assert np.array_equal(q[i, 16 * blk:16 * blk + 16], packed)
+
+
+def test_append_nothing(cuda):
+    cache = sentinel_cache(1, 2, 16, 64, fp4.NVFP4, cuda)
+    e = torch.empty((0, 2, 64), dtype=torch.bfloat16, device=cuda)
+    fp4.fp4_kv_append(e, e, cache, torch.empty(0, dtype=torch.int64, device=cuda), **scales_for(fp4.NVFP4, cuda))
+    assert all(bool((t == SENTINEL).all()) for t in cache)
+
+
+# ---------------------------------------------------------------------------------------------
+# read
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lens,heads,dim,page", [([1], 1, 64, 16), ([517], 8, 128, 16), ([33, 0, 100, 1, 64], 3, 64, 32),
+                                                 ([200, 129], 2, 128, 128)])
+def test_read_values(cuda, fmt, dtype, lens, heads, dim, page):
+    c = Cache(lens, heads, dim, page, FORMATS[fmt])
+    starts = [min(3, n) for n in lens]
+    rows = [n - s for n, s in zip(lens, starts)]
+    cu = np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)
+    total = int(cu[-1])
+    pad = 5
+    outs = tuple(torch.full((total + pad, heads, dim), 7.0, dtype=dtype, device=cuda) for _ in range(2))
+    fp4.fp4_kv_read(c.arrays, c.table, torch.from_numpy(cu).to(cuda), total + pad, c.fmt,
+                    starts=torch.tensor(starts, dtype=torch.int32, device=cuda), out=outs, **c.scales)
+    for which, g in ((0, c.k_global), (1, c.v_global)):
+        assert bool((outs[which][total:] == 7.0).all())
+        at = 0
+        for b, n in enumerate(lens):
+            t = np.arange(starts[b], n)
+            pg = c.table_np[b, t // page]
+            q, s = (c.arrays_np[2 * which + i][pg, :, t % page] for i in (0, 1))
+            if len(t):
+                want = O.dequantize(q.reshape(-1, dim // 2), s.reshape(len(t) * heads, -1), c.fmt, np.float32(g)).reshape(len(t), heads, dim)
+                assert torch.equal(outs[which][at:at + len(t)].cpu(), torch.from_numpy(want).to(dtype))
+            at += len(t)
+
+
+def test_read_every_scale_byte(cuda):
+    """All 256 scale bytes: the values fp4_dequantize gives (NaN where it gives NaN)."""
+    for fmt in (fp4.NVFP4, fp4.MXFP4):
+        nb = 64 // block_of(fmt)
+        cache = fp4.fp4_kv_alloc(256 // nb, 1, 16, 64, fmt, device=cuda)
+        sb = torch.arange(256, dtype=torch.uint8).view(-1, nb)
+        cache[0][:, 0, 0] = torch.arange(32, dtype=torch.uint8).mul(0x37).to(cuda)
+        cache[1][:, 0, 0] = sb.to(cuda)
+        rows = cache[0].shape[0]
+        table = torch.arange(rows, dtype=torch.int32, device=cuda)[:, None]
+        sc = scales_for(fmt, cuda)
+        k, _ = fp4.fp4_kv_read(cache, table, torch.arange(rows + 1, dtype=torch.int32, device=cuda), rows, fmt,
+                               out_dtype=torch.float32, **sc)
+        want = fp4.fp4_dequantize(cache[0][:, 0, 0].contiguous(), cache[1][:, 0, 0].contiguous(), fmt, sc.get("k_global"))
+        assert torch.equal(k[:, 0].view(torch.int32), want.view(torch.int32)) or \
+            torch.equal(torch.nan_to_num(k[:, 0], nan=1e30), torch.nan_to_num(want, nan=1e30))
+
+
+def test_read_missing_pages_and_ranges(cuda):
+    c = Cache([70], 2, 64, 16, fp4.NVFP4)
+    table = c.table.clone()
+    table[0, 1], table[0, 3] = -1, 10 ** 6
+    cu = torch.tensor([0, 90], dtype=torch.int32, device=cuda)
+    k, v = fp4.fp4_kv_read(c.arrays, table, cu, 90, starts=torch.tensor([-4], dtype=torch.int32, device=cuda),
+                           out_dtype=torch.float32, **c.scales)
+    want, _ = fp4.fp4_kv_read(c.arrays, c.table, torch.tensor([0, 70], dtype=torch.int32, device=cuda), 70,
+                              out_dtype=torch.float32, **c.scales)
+    t = np.arange(-4, 86)
+    zero = (t < 0) | (t >= 80) | ((t >= 16) & (t < 32)) | ((t >= 48) & (t < 64))
+    kk = k.cpu().numpy()
+    assert (kk[zero] == 0).all() and (v.cpu().numpy()[zero] == 0).all()
+    seen = ~zero & (t < 70)
+    assert np.array_equal(kk[seen], want.cpu().numpy()[t[seen]])
+
+
+# ---------------------------------------------------------------------------------------------
+# attention
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("group", [1, 3, 8, 16])
+@pytest.mark.parametrize("lens,page", [([1], 16), ([15, 16, 17], 16), ([300, 1, 0, 129], 32), ([64, 65, 1000], 64)])
+def test_decode(cuda, fmt, dim, group, lens, page):
+    c = Cache(lens, 2, dim, page, FORMATS[fmt], seed=group)
+    run_and_check(c, [1] * len(lens), group, uniform=True)
+
+
+@pytest.mark.parametrize("heads,group,lens", [(1, 8, [9000]), (8, 1, [40] * 70), (3, 7, [2500, 100, 1, 700]), (1, 1, [5000]),
+                                              (2, 32, [1500]), (1, 71, [333, 20])])
+def test_decode_splits(cuda, heads, group, lens):
+    """One long sequence over many blocks, many short ones in few, ragged mixes."""
+    c = Cache(lens, heads, 128, 64, fp4.NVFP4, seed=5)
+    run_and_check(c, [1] * len(lens), group, strided=True)
+
+
+@pytest.mark.parametrize("window", [1, 7, 64, 130, 5000])
+@pytest.mark.parametrize("causal", [True, False])
+def test_window(cuda, window, causal):
+    c = Cache([700, 64, 33, 129], 2, 64, 16, fp4.MXFP4, seed=2)
+    run_and_check(c, [1, 5, 33, 12], 4, causal=causal, window=window)
+
+
+@pytest.mark.parametrize("fmt,dim,page", [("nvfp4", 128, 32), ("mxfp4", 64, 16), ("mxfp4", 128, 256), ("nvfp4", 64, 64)])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("queries,lens,group", [
+    ([2, 5, 1, 8], [100, 5, 77, 900], 4), ([17, 40], [300, 40], 1), ([129, 64, 1, 0], [129, 500, 200, 3], 5),
+    ([257], [700], 8), ([31, 130], [31, 130], 16)])
+def test_several_queries(cuda, fmt, dim, page, causal, queries, lens, group):
+    c = Cache(lens, 2, dim, page, FORMATS[fmt], seed=9)
+    run_and_check(c, queries, group, causal=causal, strided=True, pad_rows=3)
+
+
+def test_long_prompt_rows(cuda):
+    """A prompt longer than any tile, checked on every row."""
+    c = Cache([1500], 1, 128, 64, fp4.NVFP4, seed=4)
+    run_and_check(c, [1500], 2)
+    run_and_check(c, [600], 3, window=200)
+
+
+def test_more_queries_than_keys(cuda):
+    """Queries before the first key see nothing: zeros and -inf."""
+    c = Cache([5, 0, 40], 2, 64, 16, fp4.NVFP4)
+    out, lse = run_and_check(c, [9, 3, 70], 4)
+    assert bool((out[:4] == 0).all()) and bool(torch.isneginf(lse[:4]).all())
+    assert bool((out[9:12] == 0).all()) and bool(torch.isneginf(lse[9:12]).all())
+
+
+@pytest.mark.parametrize("queries", [1, 3, 40])
+def test_missing_pages_are_not_seen(cuda, queries):
+    """Entries outside the cache hold no tokens, wherever they sit; a sequence of nothing else is empty."""
+    c = Cache([200, 90, 64], 2, 64, 16, fp4.NVFP4, seed=3)
+    gone = [np.zeros(n, dtype=bool) for n in c.lens]
+    table = c.table.clone()
+    for b, p, bad in ((0, 0, -1), (0, 5, 10 ** 6), (0, 12, -7), (1, 5, -1), *((2, p, -1) for p in range(4))):
+        table[b, p] = bad
+        gone[b][16 * p:16 * p + 16] = True
+    c.table = table
+    out, lse = run_and_check(c, [queries] * 3, 4, gone=gone)
+    assert bool((out[2 * queries:] == 0).all()) and bool(torch.isneginf(lse[2 * queries:]).all())
+
+
+@pytest.mark.parametrize("queries", [1, 40])
+def test_lengths_beyond_the_table(cuda, queries):
+    """lens past the table's pages count as the table's; negative as none."""
+    c = Cache([64, 64], 1, 64, 16, fp4.NVFP4, extra_cols=0)
+    c.lens_t = torch.tensor([10 ** 6, -3], dtype=torch.int32, device="cuda")
+    c.lens = [64, 0]
+    c.k64[1], c.v64[1] = c.k64[1][:0], c.v64[1][:0]
+    run_and_check(c, [queries] * 2, 4)
+
+
+@pytest.mark.parametrize("queries", [1, 48])
+@pytest.mark.parametrize("spread", [1e-6, 40.0])
+def test_extreme_scores(cuda, queries, spread):
+    """Almost uniform weights, and weights of almost one key (scores of thousands)."""
+    c = Cache([777], 1, 128, 16, fp4.NVFP4, seed=6)
+    run_and_check(c, [queries], 8, q_spread=spread)
+
+
+@pytest.mark.parametrize("queries", [1, 48])
+def test_query_range(cuda, queries):
+    """Queries of very large and very small magnitude, within a row too: bf16 far outside fp16's range."""
+    c = Cache([200], 1, 64, 16, fp4.NVFP4, seed=8)
+    g = torch.Generator().manual_seed(1)
+    q = torch.randn(queries, 4, 64, generator=g)
+    q = q * torch.tensor([2.0 ** 100, 2.0 ** -100, 1.0, 1.0])[None, :, None]
+    q[:, 2, ::2] *= 2.0 ** -20
+    q = q.to(torch.bfloat16)
+    for h, scale in ((0, 2.0 ** -103), (1, 2.0 ** 97), (2, 0.125), (3, -0.125)):
+        out, lse = fp4.fp4_kv_attention(q[:, h:h + 1].to(cuda), c.arrays, c.table, c.lens_t, max_q=queries, scale=scale,
+                                        want_lse=True, **c.scales)
+        ref = attention64(q[:, h:h + 1].double().numpy(), c.k64[0], c.v64[0], scale, True, 0)
+        check(out, lse, ref, 200, 64, np.abs(c.v64[0]).max())
+
+
+@pytest.mark.parametrize("queries", [1, 48])
+def test_zero_queries_and_zero_scale(cuda, queries):
+    c = Cache([100], 1, 64, 16, fp4.MXFP4)
+    run_and_check(c, [queries], 2, q_spread=0.0)
+    run_and_check(c, [queries], 2, scale=0.0)
+
+
+@pytest.mark.parametrize("queries", [1, 40, 90])
+def test_nan_scale_bytes(cuda, queries):
+    """The scale byte of a key as NaN: NaN in the rows that see the token and in no other.  Of a value
+    block: as zero."""
+    c = Cache([100, 100], 1, 64, 16, fp4.NVFP4)
+    q = torch.randn(2 * queries, 4, 64, device=cuda).to(torch.bfloat16)
+    sees = torch.arange(100 - queries, 100, device=cuda) >= 37
+
+    def run(which, byte):
+        arrays = [a.clone() for a in c.arrays]
+        arrays[which][int(c.table_np[0, 2]), 0, 5, 1] = byte   # token 37 of sequence 0
+        return fp4.fp4_kv_attention(q, arrays, c.table, c.lens_t, max_q=queries, want_lse=True, **c.scales)
+
+    out, lse = run(1, 0x7F)
+    assert bool(torch.isnan(out[:queries].float())[sees].all()) and bool(torch.isnan(lse[:queries][sees]).all())
+    good, good_lse = run(1, 0x30)
+    assert torch.equal(out[queries:], good[queries:]) and torch.equal(lse[queries:], good_lse[queries:])
+    assert torch.equal(out[:queries][~sees], good[:queries][~sees])
+    out, lse = run(3, 0x7F)
+    good, good_lse = run(3, 0x00)
+    assert torch.equal(out, good) and torch.equal(lse, good_lse)
+
+
+def test_max_q_bounds_the_work(cuda):
+    """Queries beyond max_q of a sequence are not computed; their rows stay."""
+    c = Cache([50, 60], 1, 64, 16, fp4.NVFP4)
+    q = torch.randn(9, 2, 64, device=cuda).to(torch.bfloat16)
+    cu = torch.tensor([0, 6, 9], dtype=torch.int32, device=cuda)
+    full, _ = fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, cu_q=cu, max_q=6, **c.scales)
+    out = torch.full_like(full, 7.0)
+    fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, cu_q=cu, max_q=4, out=out, **c.scales)
+    assert bool((out[4:6] == 7.0).all()) and torch.equal(out[:4], full[:4]) and torch.equal(out[6:], full[6:])
+
+
+# ---------------------------------------------------------------------------------------------
+# the operators together, streams, graphs
+
+def test_serving_loop(cuda):
+    """A prompt in two chunks, then single tokens, each step append + attention, against the formula on
+    what the cache reads back."""
+    heads, group, dim, page, seqs = 2, 4, 64, 16, 3
+    rng = torch.Generator(device=cuda).manual_seed(0)
+    cache = sentinel_cache(40, heads, page, dim, fp4.NVFP4, cuda)
+    table = torch.randperm(36, generator=rng, device=cuda).to(torch.int32).view(seqs, 12)
+    sc = scales_for(fp4.NVFP4, cuda)
+    lens = [0] * seqs
+    for new in ([30, 1, 47], [50, 20, 3], [1, 1, 1], [1, 1, 1], [4, 1, 2]):
+        total = sum(new)
+        qkv = torch.randn(total, (group + 2) * heads, dim, generator=rng, device=cuda).to(torch.bfloat16)
+        seq = np.repeat(np.arange(seqs), new)
+        token = np.concatenate([np.arange(n, n + m) for n, m in zip(lens, new)])
+        slots = table.cpu().numpy()[seq, token // page].astype(np.int64) * page + token % page
+        fp4.fp4_kv_append(qkv[:, group * heads:(group + 1) * heads], qkv[:, (group + 1) * heads:], cache,
+                          torch.from_numpy(slots).to(cuda), **sc)
+        lens = [n + m for n, m in zip(lens, new)]
+        cu = torch.tensor(np.concatenate([[0], np.cumsum(new)]), dtype=torch.int32, device=cuda)
+        lt = torch.tensor(lens, dtype=torch.int32, device=cuda)
+        out, lse = fp4.fp4_kv_attention(qkv[:, :group * heads], cache, table, lt, cu_q=cu, max_q=max(new), want_lse=True, **sc)
+        ck = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=cuda)
+        k, v = fp4.fp4_kv_read(cache, table, ck, sum(lens), out_dtype=torch.float32, **sc)
+        at = ak = 0
+        for n, m in zip(lens, new):
+            kk, vv = k[ak:ak + n].cpu().double().numpy(), v[ak:ak + n].cpu().double().numpy()
+            ref = attention64(qkv[at:at + m, :group * heads].cpu().double().numpy(), kk, vv, dim ** -0.5, True, 0)
+            check(out[at:at + m], lse[at:at + m], ref, n, dim, np.abs(vv).max())
+            at, ak = at + m, ak + n
+
+
+def _decode_case(cuda, seed, lens, page=16):
+    c = Cache(lens, 2, 128, page, fp4.NVFP4, seed=seed)
+    q = torch.randn(len(lens), 8, 128, device=cuda, generator=torch.Generator(device=cuda).manual_seed(seed)).to(torch.bfloat16)
+    return c, q
+
+
+def test_other_stream_and_repeatability(cuda):
+    c, q = _decode_case(cuda, 1, [3000, 17, 900])
+    want, lse = fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, want_lse=True, **c.scales)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        out, l2 = fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, want_lse=True, stream=side, **c.scales)
+        side.synchronize()
+        assert torch.equal(out, want) and torch.equal(l2, lse)
+
+
+def test_graphs_replay_with_new_lengths(cuda):
+    """Two captured decode steps, replayed at once on two streams with lengths changed after capture."""
+    cases = [_decode_case(cuda, s, [2000, 64, 700]) for s in (1, 2)]
+    graphs, outs = [], []
+    for c, q in cases:
+        fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, **c.scales)
+    torch.cuda.synchronize()
+    for c, q in cases:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, **c.scales)[0])
+        graphs.append(g)
+    new = [1500, 3, 699]
+    for c, _ in cases:
+        c.lens_t.copy_(torch.tensor(new, dtype=torch.int32))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for s, g in zip(streams, graphs):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for (c, q), out in zip(cases, outs):
+        want, _ = fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, **c.scales)
+        assert torch.equal(out, want)
+
+
+def test_offsets_beyond_32_bits(cuda):
+    """A cache of more than 2^32 bytes an array: pages at both ends give the same rows."""
+    heads, page, dim = 8, 1024, 128
+    pages = (2 ** 32) // (heads * page * (dim // 2)) + 2
+    cache = tuple(torch.empty((pages, heads, page, n), dtype=torch.uint8, device=cuda) for n in (64, 8, 64, 8))
+    sc = scales_for(fp4.NVFP4, cuda)
+    x = torch.randn(2, 20, heads, dim, device=cuda).to(torch.bfloat16)
+    tables = {}
+    for name, p in (("low", 0), ("high", pages - 1)):
+        slots = torch.arange(20, device=cuda) + p * page
+        fp4.fp4_kv_append(x[0], x[1], cache, slots, **sc)
+        tables[name] = torch.tensor([[p]], dtype=torch.int32, device=cuda)
+    q = torch.randn(20, 16, dim, device=cuda).to(torch.bfloat16)
+    n = torch.tensor([20], dtype=torch.int32, device=cuda)
+    cu = torch.tensor([0, 20], dtype=torch.int32, device=cuda)
+    for m in (1, 20):
+        a, b = (fp4.fp4_kv_attention(q[:m], cache, t, n, max_q=m, **sc)[0] for t in tables.values())
+        assert torch.equal(a, b) and bool(torch.isfinite(a.float()).all())
+    a, b = (fp4.fp4_kv_read(cache, t, cu, 20, **sc)[0] for t in tables.values())
+    assert torch.equal(a, b)
+    want, _ = quantise(x[0].float().cpu().numpy(), fp4.NVFP4, 0.0021)
+    assert np.array_equal(cache[0][pages - 1, :, :20].transpose(0, 1).cpu().numpy(), want)
