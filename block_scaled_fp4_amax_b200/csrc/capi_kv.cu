@@ -141,6 +141,9 @@ fp4_status fp4_kv_attention(const void* q, fp4_dtype dtype, long total_q, long q
     return kv_fail(FP4_EINVAL, "q_heads %d must be a multiple of heads %d, at most 4096", q_heads, heads);
   if (total_q < 0 || total_q > (1L << 24)) return kv_fail(FP4_EINVAL, "total_q %ld outside 0 .. 2^24", total_q);
   if (!std::isfinite(scale)) return kv_fail(FP4_EINVAL, "scale must be finite");
+  if (seqs > 32768) return kv_fail(FP4_EUNSUPPORTED, "seqs %d above 32768", seqs);
+  if ((long long)max_pages * page_size > (1LL << 30))
+    return kv_fail(FP4_EUNSUPPORTED, "a block table of more than 2^30 tokens a sequence");
   if (window < 0) return kv_fail(FP4_EINVAL, "window %d is negative (0: no window)", window);
   if (total_q == 0 || seqs == 0) return FP4_OK;
   if (max_q < 1) return kv_fail(FP4_EINVAL, "max_q %d must be positive", max_q);
@@ -154,7 +157,8 @@ fp4_status fp4_kv_attention(const void* q, fp4_dtype dtype, long total_q, long q
     return kv_fail(FP4_EINVAL, "a 16-byte aligned workspace of %zu bytes is required", need);
   L.q = q; L.q_stride = q_stride; L.q_head_stride = q_head_stride; L.total_q = total_q; L.q_heads = q_heads;
   L.table = table; L.table_stride = table_stride; L.max_pages = max_pages; L.seqs = seqs;
-  L.cu_q = cu_q; L.max_q = max_q; L.lens = lens; L.scale = scale; L.causal = causal != 0; L.window = window;
+  L.cu_q = cu_q; L.max_q = max_q; L.lens = lens; L.scale = scale; L.causal = causal != 0;
+  L.window = window > (1 << 30) ? 0 : window;  // wider than any sequence: none
   L.out = out; L.lse = lse; L.workspace = workspace;
   return kv_launched(fp4k::launch_kv_attention(L, static_cast<cudaStream_t>(stream)), "fp4_kv_attention");
 }

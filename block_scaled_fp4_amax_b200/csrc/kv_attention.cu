@@ -112,9 +112,10 @@ __global__ void __launch_bounds__(32 * kWarps) kv_attention_kernel(AttnParams p)
 
 }  // namespace
 
-size_t kv_attention_workspace() { return 16; }
+size_t kv_attention_workspace() { return kv_decode_workspace(); }
 
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t s) {
+  if ((long long)L.max_q * (L.q_heads / L.c.heads) <= 32) return launch_kv_decode(L, s);
   AttnParams p{L, L.q_heads / L.c.heads};
   const unsigned grid = (unsigned)((L.total_q * L.q_heads + kWarps - 1) / kWarps);
   if (L.c.head_dim == 128) {

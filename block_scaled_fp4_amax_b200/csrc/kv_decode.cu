@@ -1,0 +1,505 @@
+// kv_decode.cu — attention over the paged 4-bit cache for a few query rows a key/value head: one new
+// token a sequence, or a handful of drafted ones (rows = queries x query heads of a key/value head).
+//
+// The cache is read once, so the work is bound by its bytes (144 a token and head at head_dim 128)
+// as long as unpacking keeps up: 1.5 instructions a value.  A unit of work is one (sequence, head).
+// All units' tiles of 64 tokens are laid end to end, and CTA i of n takes tiles [i T / n, (i + 1) T / n),
+// whatever the lengths (which only the device knows), so every CTA has the same number of tiles; a
+// unit that falls into several CTAs is written as fp32 partial results that a second, small launch
+// joins (launched programmatically: it is resident when the first one drains).
+//
+// Inside a CTA each of the four warps takes 16 tokens of a tile and keeps its own running maximum,
+// sum and output; they meet once at the end of a unit.  Bytes come through a ring of cp.async
+// stages per warp (no CTA barrier in the loop) and are expanded in registers, straight into the
+// fragments of mma.m16n8k16 (f16 x f16 + f32):
+//   S^T = K Q^T: 16 tokens x 8 rows per MMA.  The order of the summed channels is free, so thread t of
+//     a row's four takes the channels [t D/4, (t + 1) D/4) as they lie in memory, one 16-byte load.
+//   O^T += V^T P: 16 channels x 8 rows.  Thread g takes the channels [g D/8, (g + 1) D/8) of four
+//     tokens; the order of tokens is the one P's fragments have after an 8x8 transpose.
+// Values v * d (E2M1 times block scale) are exact in fp16; the per-tensor scales act on the fp32 sums.
+// Queries are scaled per row by a power of two so that fp16 holds their bf16 values exactly.  Weights
+// exp2(z - m + 7) are rounded to fp16 for the product (m is the running maximum; it is raised only
+// when a score passes it by 8, so weights stay below 2^15 and 2^-29 of the largest keeps full
+// precision) and summed unrounded.
+#include "fp4_device.cuh"
+#include "kv_attention.cuh"
+#include "launch.h"
+
+namespace fp4k {
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kTile = 16 * kWarps;  // tokens of a CTA step
+constexpr int kStages = 4;
+
+// Rows a CTA handles (8 per n-tile) and CTAs per SM.
+template <int NT> struct DecodeCfg {
+  static constexpr int kCtas = NT == 1 ? 4 : (NT == 2 ? 3 : 2);
+};
+
+constexpr int kMaxCtasPerSm = 4;
+// Rows of partial results an SM's CTAs may leave: two slots a CTA, 8 NT rows a slot.
+constexpr int kPartRowsPerSm = 2 * 2 * 32;
+static_assert(DecodeCfg<1>::kCtas * 16 <= kPartRowsPerSm && DecodeCfg<2>::kCtas * 32 <= kPartRowsPerSm &&
+              DecodeCfg<4>::kCtas * 64 <= kPartRowsPerSm && DecodeCfg<1>::kCtas <= kMaxCtasPerSm, "workspace");
+
+struct DecodeParams {
+  KvAttentionLaunch a;
+  int group;       // query heads of a key/value head
+  int chunk_seqs;  // sequences of a blockIdx.y
+  float* part;     // partial outputs, [slot][row][D]
+  float2* part_ml; // their maximum and sum, [slot][row]
+  KvJoin* joins;   // one per CTA
+};
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+__device__ __forceinline__ void mma_f16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+  return r;
+}
+
+template <int D, bool NV>
+struct StageCfg {
+  static constexpr int B = NV ? 16 : 32;
+  static constexpr int kQ = 16 * D / 2;   // nibble bytes of 16 tokens
+  static constexpr int kS = 16 * (D / B); // scale bytes
+  static constexpr int kBytes = 2 * kQ + 2 * kS;
+};
+
+template <int D, bool NV, int NT>
+constexpr int decode_smem() {
+  // rings, then the merge area: [warp][row][D + 4] outputs and [warp][row] maxima and sums
+  return kWarps * kStages * StageCfg<D, NV>::kBytes + kWarps * 8 * NT * (D + 4) * 4 + kWarps * 8 * NT * 8;
+}
+
+template <int D, bool NV, int NT>
+__global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_kernel(DecodeParams p) {
+  using S = StageCfg<D, NV>;
+  constexpr int B = S::B, NB = D / B;
+  constexpr int MT = D / 16;    // 16-channel tiles of the output
+  constexpr int KW = D / 32;    // packed words of a thread's channels of one key (D / 4 values)
+  constexpr int VW = D / 64;    // packed words of a thread's channels of one value (D / 8 values)
+  constexpr int LD = D + 4;     // merge row, padded so that a fragment store meets no bank twice
+  extern __shared__ __align__(16) uint8_t smem[];
+  __shared__ KvSchedule sched;
+
+  const KvAttentionLaunch& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+  uint8_t* ring = smem + warp * kStages * S::kBytes;
+  float* merge = reinterpret_cast<float*>(smem + kWarps * kStages * S::kBytes);
+  float2* merge_ml = reinterpret_cast<float2*>(merge + kWarps * 8 * NT * LD);
+
+  grid_dep_trigger();
+  const int seq0 = blockIdx.y * p.chunk_seqs, nseq = min(p.chunk_seqs, a.seqs - seq0);
+  kv_schedule<kTile, 32 * kWarps>(a, seq0, nseq, sched);
+  const long long total = sched.prefix[nseq] * a.c.heads;
+  const int cta = blockIdx.x;
+  const long long n = min((long long)gridDim.x, total);  // every CTA that works has a tile
+  const long long x0 = cta < n ? cta * total / n : 0, x1 = cta < n ? (cta + 1) * total / n : 0;
+  KvJoin join = {0, 0, 0, 0};
+
+  // The cursor that fills the ring runs ahead of the one that consumes it, across units.
+  KvCursor fill, use;
+  kv_seek<kTile>(a, fill, sched, seq0, nseq, x0);
+  use = fill;
+  const uint32_t row_bytes = D / 2;
+  const int my16 = 16 * warp;
+  long long fx = x0;
+  // page ids of this warp's next 32 tiles of the current unit, one a lane
+  int ids = -1, ids_tile = -1;
+  uint32_t absent = 0u;  // bit i: stage i holds tokens without a page (zeros)
+
+  auto fetch = [&](int stage) {
+    if (fx >= x1) { cp_commit(); return; }
+    if (ids_tile < 0 || fill.tile - ids_tile >= 32) {
+      ids_tile = fill.tile;
+      const long long j = (long long)(fill.first + fill.tile + lane) * kTile + my16;
+      const long long pg = j >> a.c.page_shift;
+      ids = pg < a.max_pages ? __ldg(a.table + (seq0 + fill.seq) * a.table_stride + pg) : -1;
+    }
+    const int page = __shfl_sync(0xFFFFFFFFu, ids, fill.tile - ids_tile);
+    const bool live = page >= 0 && page < a.c.num_pages;
+    const int j = (fill.first + fill.tile) * kTile + my16;
+    const long long row = (((long long)(live ? page : 0) * a.c.heads + fill.head) << a.c.page_shift) +
+                          (j & ((1 << a.c.page_shift) - 1));
+    const uint32_t dst = smem_addr(ring + stage * S::kBytes);
+    const uint8_t* kq = a.c.kq + row * row_bytes;
+    const uint8_t* vq = a.c.vq + row * row_bytes;
+#pragma unroll
+    for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + 512 * i + 16 * lane, kq + 512 * i + 16 * lane, live);
+#pragma unroll
+    for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + S::kQ + 512 * i + 16 * lane, vq + 512 * i + 16 * lane, live);
+    constexpr int SL = S::kS / 16;  // lanes that copy the scales of one array
+    if (lane < 2 * SL) {
+      const uint8_t* s = (lane < SL ? a.c.ks : a.c.vs) + row * NB;
+      cp_async16(dst + 2 * S::kQ + 16 * lane, s + 16 * (lane < SL ? lane : lane - SL), live);
+    }
+    cp_commit();
+    absent = live ? absent & ~(1u << stage) : absent | (1u << stage);
+    ++fx;
+    if (++fill.tile == fill.tiles) {
+      kv_next<kTile>(a, fill, sched, seq0, nseq);
+      ids_tile = -1;
+    }
+  };
+
+#pragma unroll
+  for (int i = 0; i < kStages - 1; ++i) fetch(i);
+  int stage = 0;
+
+  for (long long x = x0; x < x1;) {
+    // ---------------------------------------------------------------- one unit, or the part of it here
+    const int seq = seq0 + use.seq, head = use.head;
+    const KvSpan span = kv_span(a, seq);
+    const int rows = span.queries * p.group;
+    const int tile0 = use.tile;
+    const int tile1 = (int)min((long long)use.tiles, tile0 + (x1 - x));
+
+    // queries: row 8 n + g, channels [t D/4, (t + 1) D/4), as fp16 fragments
+    uint32_t qf[NT][D / 8];
+    float coef[NT];  // of row 8 n + g: score in log2 units = sum * coef
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = 8 * nt + g;
+      uint32_t raw[D / 8];
+      uint32_t m = 0u;
+      const bool have = r < rows;
+      const int qi = have ? r / p.group : 0;
+      const char* src = reinterpret_cast<const char*>(a.q) +
+                        2 * ((span.first_q + qi) * a.q_stride + (long long)(head * p.group + (have ? r - qi * p.group : 0)) * a.q_head_stride + t * (D / 4));
+#pragma unroll
+      for (int i = 0; i < D / 32; ++i) {
+        uint4 v = make_uint4(0u, 0u, 0u, 0u);
+        if (have) v = __ldg(reinterpret_cast<const uint4*>(src) + i);
+        raw[4 * i] = v.x; raw[4 * i + 1] = v.y; raw[4 * i + 2] = v.z; raw[4 * i + 3] = v.w;
+      }
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) m = max(m, max((raw[i] & 0x7FFFu) << 16, raw[i] & 0x7FFF0000u));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 1));
+      m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
+      float up, down;
+      kv_query_scale(m, up, down);
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i)
+        qf[nt][i] = f16x2_pack(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xFFFF0000u) * up);
+      coef[nt] = a.scale * 1.44269504f * (NV ? __ldg(a.c.k_global) : 1.0f) * down;
+    }
+    // the coefficients of this lane's score columns (rows 8 n + 2 t and 8 n + 2 t + 1)
+    float cz[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      cz[nt][0] = __shfl_sync(0xFFFFFFFFu, coef[nt], 8 * t);
+      cz[nt][1] = __shfl_sync(0xFFFFFFFFu, coef[nt], 8 * t + 4);
+    }
+
+    float o[NT][MT][4], mx[NT][2], sum[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      mx[nt][0] = mx[nt][1] = kNoMax;
+      sum[nt][0] = sum[nt][1] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) o[nt][i][c] = 0.0f;
+    }
+
+    for (int tile = tile0; tile < tile1; ++tile) {
+      fetch(stage == 0 ? kStages - 1 : stage - 1);
+      cp_wait<kStages - 1>();
+      __syncwarp();
+      const uint8_t* st = ring + stage * S::kBytes;
+      const bool live = !((absent >> stage) & 1u);
+      stage = stage == kStages - 1 ? 0 : stage + 1;
+      // MMA row r holds token r ^ ((r >> 1) & 1): the values' loads of four threads then fall on both
+      // halves of the banks
+      const int tok = g ^ ((g >> 1) & 1);
+
+      // ---- scores
+      float s[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
+      {
+        uint32_t kw[2][KW];
+        uint32_t ks2[2][2];  // the scales of the thread's channels (first and second half of them), doubled
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* src = st + (tok + 8 * u) * row_bytes + t * (D / 8);
+          if constexpr (KW == 4) {
+            const uint4 w = *reinterpret_cast<const uint4*>(src);
+            kw[u][0] = w.x; kw[u][1] = w.y; kw[u][2] = w.z; kw[u][3] = w.w;
+          } else {
+            const uint2 w = *reinterpret_cast<const uint2*>(src);
+            kw[u][0] = w.x; kw[u][1] = w.y;
+          }
+          const uint8_t* sc = st + 2 * S::kQ + (tok + 8 * u) * NB;
+          if constexpr (NV && D == 128) {
+            const uint32_t two = e4m3x2_to_f16x2(*reinterpret_cast<const uint16_t*>(sc + 2 * t));
+            ks2[u][0] = __byte_perm(two, two, 0x1010);
+            ks2[u][1] = __byte_perm(two, two, 0x3232);
+          } else {
+            ks2[u][0] = ks2[u][1] = kv_scale_f16x2<NV>(sc[t * (D / 4) / B]);
+          }
+        }
+        float s2[NT][4];  // a second chain of sums: half the latency of one
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s2[nt][0] = s2[nt][1] = s2[nt][2] = s2[nt][3] = 0.0f;
+#pragma unroll
+        for (int w = 0; w < KW; ++w) {
+          uint32_t h[2][4];
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            e2m1x8_to_f16x2(kw[u][w], h[u]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[u][i] = f16x2_mul(h[u][i], ks2[u][w / (KW / 2)]);
+          }
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const uint32_t af[4] = {h[0][2 * i], h[1][2 * i], h[0][2 * i + 1], h[1][2 * i + 1]};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(i == 0 ? s[nt] : s2[nt], af, qf[nt][4 * w + 2 * i], qf[nt][4 * w + 2 * i + 1]);
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) s[nt][c] = (s[nt][c] + s2[nt][c]) * cz[nt][c & 1];
+      }
+
+      // ---- mask: only where some row's range ends inside the 16 tokens, or a page is missing
+      const int j0 = (use.first + tile) * kTile + my16;
+      if (!(live && j0 >= span.lo_all && j0 + 16 <= span.hi_all)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int r = 8 * nt + 2 * t + (c & 1), j = j0 + tok + (c >= 2 ? 8 : 0);
+            int lo, hi;
+            kv_row_range(a, span, r / p.group, lo, hi);
+            if (!(live && j >= lo && j < hi)) s[nt][c] = -INFINITY;
+          }
+      }
+
+      // ---- running maximum (raised rarely), weights, sums
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) raise |= fmaxf(s[nt][c], s[nt][c + 2]) > mx[nt][c] + kRaise;
+      if (__any_sync(0xFFFFFFFFu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float m = fmaxf(s[nt][c], s[nt][c + 2]);
+#pragma unroll
+            for (int x2 = 4; x2 < 32; x2 <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x2));
+            m = fmaxf(m, mx[nt][c]);
+            const float f = exp2_approx(mx[nt][c] - m);
+            mx[nt][c] = m;
+            sum[nt][c] *= f;
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+              o[nt][i][c] *= f;
+              o[nt][i][c + 2] *= f;
+            }
+          }
+      }
+      uint32_t pf[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          w[c] = exp2_approx(s[nt][c] - (mx[nt][c & 1] - kShift));
+          sum[nt][c & 1] += w[c];
+        }
+        pf[nt][0] = transpose8x8(f16x2_pack(w[0], w[1]));
+        pf[nt][1] = transpose8x8(f16x2_pack(w[2], w[3]));
+      }
+
+      // ---- weighted sum of the values: tokens tA, tB (fragment columns 2 t, 2 t + 1) and 8 further on
+      {
+        const int tA = 2 * t + (t & 1), tB = 2 * t + 1 - (t & 1);
+        uint32_t vw[4][VW], vs2[2];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          const int tk = ((u & 1) ? tB : tA) + (u >= 2 ? 8 : 0);
+          const uint8_t* src = st + S::kQ + tk * row_bytes + g * (D / 16);
+          if constexpr (VW == 2) {
+            const uint2 w = *reinterpret_cast<const uint2*>(src);
+            vw[u][0] = w.x; vw[u][1] = w.y;
+          } else {
+            vw[u][0] = *reinterpret_cast<const uint32_t*>(src);
+          }
+        }
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+          const uint8_t* sc = st + 2 * S::kQ + S::kS + g * (D / 8) / B;
+          vs2[u] = kv_value_scales<NV>(sc[(tA + 8 * u) * NB], sc[(tB + 8 * u) * NB]);
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w) {
+          uint32_t h[4][4];
+#pragma unroll
+          for (int u = 0; u < 4; ++u) e2m1x8_to_f16x2(vw[u][w], h[u]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t af[4];
+            af[0] = f16x2_mul(__byte_perm(h[0][i], h[1][i], 0x5410), vs2[0]);
+            af[1] = f16x2_mul(__byte_perm(h[0][i], h[1][i], 0x7632), vs2[0]);
+            af[2] = f16x2_mul(__byte_perm(h[2][i], h[3][i], 0x5410), vs2[1]);
+            af[3] = f16x2_mul(__byte_perm(h[2][i], h[3][i], 0x7632), vs2[1]);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][4 * w + i], af, pf[nt][0], pf[nt][1]);
+          }
+        }
+      }
+      __syncwarp();  // the stage may be refilled
+    }
+
+    // ---------------------------------------------------------------- join the four warps
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+#pragma unroll
+        for (int x2 = 4; x2 < 32; x2 <<= 1) sum[nt][c] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][c], x2);
+        if (g == 0) merge_ml[warp * 8 * NT + 8 * nt + 2 * t + c] = make_float2(mx[nt][c], sum[nt][c]);
+        float* dst = merge + (warp * 8 * NT + 8 * nt + 2 * t + c) * LD + 2 * g;
+#pragma unroll
+        for (int i = 0; i < MT; ++i) *reinterpret_cast<float2*>(dst + 16 * i) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
+      }
+    __syncthreads();
+    const bool head_part = tile0 > 0, tail_part = tile1 < use.tiles;
+    const bool part = head_part || tail_part;
+    // a CTA's first part goes to slot 0, a later one (the last unit's) to slot 1
+    const long long slot = 2LL * (blockIdx.y * gridDim.x + cta) + (x == x0 ? 0 : 1);
+    const float gv = NV ? __ldg(a.c.v_global) : 1.0f;
+    constexpr int PAIRS = D / 2;
+    for (int i = threadIdx.x; i < rows * PAIRS; i += 32 * kWarps) {
+      const int r = i / PAIRS, d2 = i % PAIRS;  // channels 2 d2, 2 d2 + 1
+      const int at = (d2 % (D / 16)) * 16 + 2 * (d2 / (D / 16));
+      float m = kNoMax;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, merge_ml[w * 8 * NT + r].x);
+      float l = 0.0f, v0 = 0.0f, v1 = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float2 ml = merge_ml[w * 8 * NT + r];
+        const float f = exp2_approx(ml.x - m);
+        const float2 v = *reinterpret_cast<const float2*>(merge + (w * 8 * NT + r) * LD + at);
+        l += f * ml.y;
+        v0 += f * v.x;
+        v1 += f * v.y;
+      }
+      if (part) {
+        *reinterpret_cast<float2*>(p.part + (slot * 8 * NT + r) * D + 2 * d2) = make_float2(v0, v1);
+        if (d2 == 0) p.part_ml[slot * 8 * NT + r] = make_float2(m, l);
+      } else {
+        const int qi = r / p.group;
+        const long long row = (span.first_q + qi) * a.q_heads + head * p.group + (r - qi * p.group);
+        const float inv = kv_inverse(l) * gv;
+        reinterpret_cast<uint32_t*>(a.out)[row * PAIRS + d2] = bf16x2_pack(v0 * inv, v1 * inv);
+        if (a.lse && d2 == 0) a.lse[row] = kv_lse(m, l);
+      }
+    }
+    if (tail_part && !head_part) {
+      // this CTA holds the unit's first part: how many CTAs hold the rest, for the joining launch
+      const long long end = x + (use.tiles - tile0);  // one past the unit's last tile
+      const long long last = (end * n - 1) / total;   // the CTA that owns tile end - 1
+      join = {(int)(last - cta + 1), seq, head, (int)(slot & 1)};
+    }
+    __syncthreads();  // the merge area is free again
+    x += tile1 - tile0;
+    use.tile = tile1;
+    if (use.tile == use.tiles) kv_next<kTile>(a, use, sched, seq0, nseq);
+  }
+  if (threadIdx.x == 0) p.joins[blockIdx.y * gridDim.x + cta] = join;
+}
+
+// Joins the parts of one unit's row: part 0 lies in the slot `join.slot` of the CTA that began the
+// unit, the others in slot 0 of the CTAs after it.
+template <int D>
+__global__ void __launch_bounds__(D) kv_decode_join_kernel(DecodeParams p, int rows_cap) {
+  grid_dep_wait();
+  const KvAttentionLaunch& a = p.a;
+  const int cta = blockIdx.x, r = blockIdx.y;
+  const KvJoin join = p.joins[cta];
+  if (join.parts == 0) return;
+  const KvSpan span = kv_span(a, join.seq);
+  if (r >= span.queries * p.group) return;
+  auto at = [&](int i) { return (2LL * (cta + i) + (i == 0 ? join.slot : 0)) * rows_cap + r; };
+  float m = kNoMax;
+  for (int i = threadIdx.x & 31; i < join.parts; i += 32) m = fmaxf(m, p.part_ml[at(i)].x);
+#pragma unroll
+  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+  float l = 0.0f, v = 0.0f;
+#pragma unroll 8
+  for (int i = 0; i < join.parts; ++i) {
+    const float2 ml = p.part_ml[at(i)];
+    const float f = exp2_approx(ml.x - m);
+    l += f * ml.y;
+    v += f * p.part[at(i) * D + threadIdx.x];
+  }
+  const int qi = r / p.group;
+  const long long row = (span.first_q + qi) * a.q_heads + join.head * p.group + (r - qi * p.group);
+  const float gv = a.c.nv ? __ldg(a.c.v_global) : 1.0f;
+  reinterpret_cast<__nv_bfloat16*>(a.out)[row * D + threadIdx.x] = __float2bfloat16(v * (kv_inverse(l) * gv));
+  if (a.lse && threadIdx.x == 0) a.lse[row] = kv_lse(m, l);
+}
+
+template <int D, bool NV, int NT>
+cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
+  const int chunks = (p.a.seqs + kMaxSchedSeqs - 1) / kMaxSchedSeqs;
+  const int n = num_sms() * DecodeCfg<NT>::kCtas / chunks;  // at most 128 chunks
+  p.chunk_seqs = (p.a.seqs + chunks - 1) / chunks;
+  char* ws = static_cast<char*>(p.a.workspace);
+  p.joins = reinterpret_cast<KvJoin*>(ws);
+  ws += (size_t)num_sms() * kMaxCtasPerSm * sizeof(KvJoin);
+  p.part_ml = reinterpret_cast<float2*>(ws);
+  ws += (size_t)num_sms() * kPartRowsPerSm * sizeof(float2);
+  p.part = reinterpret_cast<float*>(ws);
+  constexpr int smem = decode_smem<D, NV, NT>();
+  cudaError_t e = cudaFuncSetAttribute(kv_decode_kernel<D, NV, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  kv_decode_kernel<D, NV, NT><<<dim3(n, chunks), 32 * kWarps, smem, s>>>(p);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const int rows = min(p.a.max_q * p.group, 8 * NT);
+  return launch_pdl(kv_decode_join_kernel<D>, dim3(n * chunks, rows), dim3(D), 0, s, true, p, 8 * NT);
+}
+
+template <int D, bool NV>
+cudaError_t decode_rows(DecodeParams& p, cudaStream_t s) {
+  const int rows = p.a.max_q * p.group;
+  if (rows <= 8) return decode_t<D, NV, 1>(p, s);
+  if (rows <= 16) return decode_t<D, NV, 2>(p, s);
+  return decode_t<D, NV, 4>(p, s);
+}
+
+}  // namespace
+
+size_t kv_decode_workspace() {
+  return (size_t)num_sms() * (kMaxCtasPerSm * sizeof(KvJoin) + kPartRowsPerSm * (sizeof(float2) + 128 * sizeof(float)));
+}
+
+cudaError_t launch_kv_decode(const KvAttentionLaunch& L, cudaStream_t s) {
+  DecodeParams p{};
+  p.a = L;
+  p.group = L.q_heads / L.c.heads;
+  if (L.c.head_dim == 128) return L.c.nv ? decode_rows<128, true>(p, s) : decode_rows<128, false>(p, s);
+  return L.c.nv ? decode_rows<64, true>(p, s) : decode_rows<64, false>(p, s);
+}
+
+}  // namespace fp4k

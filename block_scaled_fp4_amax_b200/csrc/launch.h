@@ -152,6 +152,9 @@ cudaError_t launch_kv_read(const KvReadLaunch& L, cudaStream_t s);
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t s);
 // Bytes of workspace launch_kv_attention needs on the current device.
 size_t kv_attention_workspace();
+// The kernels behind it.  launch_kv_decode: at most 32 rows (queries x query heads) a key/value head.
+cudaError_t launch_kv_decode(const KvAttentionLaunch& L, cudaStream_t s);
+size_t kv_decode_workspace();
 
 cudaError_t launch_quantize(const QuantLaunch& L, cudaStream_t s);
 // Upper bound of the tensor-amax pass's grid: the number of 32-bit slots its output needs.

@@ -376,7 +376,7 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  * Scores, softmax statistics and sums are fp32; keys and values enter the products exactly, the
  * queries too (scaled per row by a power of two), and the softmax weights, fp32 in the sum that
  * divides, are rounded to fp16 (2^-12 of each weight) for the product with V.  A query row holding
- * Inf or NaN, and an MXFP4 scale byte outside 104 .. 140, leave the rows that meet them unspecified;
+ * Inf or NaN is unspecified; an MXFP4 scale byte outside 104 .. 140 counts as the nearest of these;
  * an E4M3 NaN scale byte of a key gives NaN in the rows that see it, one of a value block counts as 0
  * (a product with a weight of 0 would carry it into rows that do not see the token).
  *   q     : device bf16 [total_q, q_heads, head_dim]; strides (elements) as in fp4_kv_append;
@@ -388,6 +388,7 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  *   lens  : device int32 [seqs]: keys of each sequence, the new tokens' included (append first);
  *           negative counts as 0, more than max_pages * page_size as that.
  *   out   : device bf16 [total_q, q_heads, head_dim], 16-byte aligned.
+ *   Limits: total_q <= 2^24, seqs <= 32768, max_pages * page_size <= 2^30, q_heads <= 4096.
  *   lse   : device float [total_q, q_heads] or NULL: natural log of the sum of exp(scale q k).
  *   workspace : device, 16-byte aligned, >= fp4_workspace_size(FP4_OP_KV_ATTENTION, total_q, q_heads)
  *           bytes; clobbered, needs no initialisation.  Calls that overlap need one each. */
