@@ -147,11 +147,17 @@ fp4_status fp4_kv_attention(const void* q, fp4_dtype dtype, long total_q, long q
   if (window < 0) return kv_fail(FP4_EINVAL, "window %d is negative (0: no window)", window);
   if (total_q == 0 || seqs == 0) return FP4_OK;
   if (max_q < 1) return kv_fail(FP4_EINVAL, "max_q %d must be positive", max_q);
+  if ((long long)max_q * (q_heads / heads) > (1LL << 30))
+    return kv_fail(FP4_EUNSUPPORTED, "max_q %d times %d query heads a head is above 2^30", max_q, q_heads / heads);
   if (!cu_q && (long long)seqs * max_q != total_q)
     return kv_fail(FP4_EINVAL, "without cu_q, total_q %ld must be seqs * max_q = %lld", total_q, (long long)seqs * max_q);
   if ((st = check_strided("q", q, q_stride, q_head_stride, 2, 16)) != FP4_OK) return st;
   if (!lens) return kv_fail(FP4_EINVAL, "NULL lens");
   if (!out || !aligned(out, 16)) return kv_fail(FP4_EINVAL, "out must be 16-byte aligned");
+  L.c.heads = heads;
+  L.q_heads = q_heads; L.max_q = max_q; L.seqs = seqs;
+  if (fp4k::kv_prompt_units(L) >= (1LL << 31))
+    return kv_fail(FP4_EUNSUPPORTED, "seqs %d times heads %d times max_q %d is more than one launch takes", seqs, heads, max_q);
   const size_t need = fp4_workspace_size(FP4_OP_KV_ATTENTION, total_q, q_heads);
   if (!workspace || ws_bytes < need || !aligned(workspace, 16))
     return kv_fail(FP4_EINVAL, "a 16-byte aligned workspace of %zu bytes is required", need);

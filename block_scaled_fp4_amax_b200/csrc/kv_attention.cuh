@@ -15,8 +15,6 @@ constexpr float kNoMax = -3e38f;
 // the largest possible one is still a normal fp16 number.
 constexpr float kRaise = 8.0f, kShift = 7.0f;
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
-
 __device__ __forceinline__ float exp2_approx(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -24,6 +24,7 @@
 #include "fp4_device.cuh"
 #include "kv_attention.cuh"
 #include "launch.h"
+#include "sm100_ptx.cuh"
 
 namespace fp4k {
 
@@ -51,6 +52,7 @@ struct DecodeParams {
   float* part;     // partial outputs, [slot][row][D]
   float2* part_ml; // their maximum and sum, [slot][row]
   KvJoin* joins;   // one per CTA
+  uint32_t* status;
 };
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
@@ -102,6 +104,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   float2* merge_ml = reinterpret_cast<float2*>(merge + kWarps * 8 * NT * LD);
 
   grid_dep_trigger();
+  if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0u;  // no wait here can give up
   const int seq0 = blockIdx.y * p.chunk_seqs, nseq = min(p.chunk_seqs, a.seqs - seq0);
   kv_schedule<kTile, 32 * kWarps>(a, seq0, nseq, sched);
   const long long total = sched.prefix[nseq] * a.c.heads;
@@ -134,7 +137,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
     const int j = (fill.first + fill.tile) * kTile + my16;
     const long long row = (((long long)(live ? page : 0) * a.c.heads + fill.head) << a.c.page_shift) +
                           (j & ((1 << a.c.page_shift) - 1));
-    const uint32_t dst = smem_addr(ring + stage * S::kBytes);
+    const uint32_t dst = smem_u32(ring + stage * S::kBytes);
     const uint8_t* kq = a.c.kq + row * row_bytes;
     const uint8_t* vq = a.c.vq + row * row_bytes;
 #pragma unroll
@@ -466,6 +469,8 @@ cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
   const int n = num_sms() * DecodeCfg<NT>::kCtas / chunks;  // at most 128 chunks
   p.chunk_seqs = (p.a.seqs + chunks - 1) / chunks;
   char* ws = static_cast<char*>(p.a.workspace);
+  p.status = reinterpret_cast<uint32_t*>(ws);
+  ws += kKvStatusBytes;
   p.joins = reinterpret_cast<KvJoin*>(ws);
   ws += (size_t)num_sms() * kMaxCtasPerSm * sizeof(KvJoin);
   p.part_ml = reinterpret_cast<float2*>(ws);

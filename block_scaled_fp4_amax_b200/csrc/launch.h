@@ -152,9 +152,15 @@ cudaError_t launch_kv_read(const KvReadLaunch& L, cudaStream_t s);
 cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t s);
 // Bytes of workspace launch_kv_attention needs on the current device.
 size_t kv_attention_workspace();
-// The kernels behind it.  launch_kv_decode: at most 32 rows (queries x query heads) a key/value head.
+// The kernels behind it.  kv_decode: at most kKvDecodeRows rows (queries x query heads) a key/value head.
+// Both keep a 32-bit status word at the start of the workspace (0: every wait ended).
+constexpr int kKvDecodeRows = 32;
+constexpr size_t kKvStatusBytes = 256;
 cudaError_t launch_kv_decode(const KvAttentionLaunch& L, cudaStream_t s);
+cudaError_t launch_kv_prompt(const KvAttentionLaunch& L, cudaStream_t s);
 size_t kv_decode_workspace();
+size_t kv_prompt_workspace();
+long long kv_prompt_units(const KvAttentionLaunch& L);  // CTAs of an unsplit launch_kv_prompt
 
 cudaError_t launch_quantize(const QuantLaunch& L, cudaStream_t s);
 // Upper bound of the tensor-amax pass's grid: the number of 32-bit slots its output needs.
@@ -184,5 +190,6 @@ cudaError_t launch_fwht_quantize(const FwhtLaunch& L, cudaStream_t s);
 cudaError_t launch_gemm(const GemmLaunch& L, cudaStream_t s);
 // Limit (ns) of each pipeline wait in GEMM launches made after the call; returns the previous one.
 unsigned long long set_gemm_wait_limit(unsigned long long ns);
+unsigned long long gemm_wait_limit();
 
 }  // namespace fp4k
