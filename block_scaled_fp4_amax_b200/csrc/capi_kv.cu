@@ -41,6 +41,8 @@ fp4_status check_cache(const unsigned char* kq, const unsigned char* ks, const u
     return kv_fail(FP4_EINVAL, "page_size %d must be a power of two in 16 .. 1024", page_size);
   if (heads < 1 || heads > 1024) return kv_fail(FP4_EINVAL, "heads %d outside 1 .. 1024", heads);
   if (num_pages < 1 || num_pages >= (1L << 31)) return kv_fail(FP4_EINVAL, "num_pages %ld outside 1 .. 2^31 - 1", num_pages);
+  if (((long long)num_pages * page_size >> 4) * heads >= (1LL << 31))
+    return kv_fail(FP4_EUNSUPPORTED, "a cache of 2^35 rows or more");
   if (!kq || !ks || !vq || !vs) return kv_fail(FP4_EINVAL, "NULL cache pointer");
   if (!aligned(kq, 16) || !aligned(ks, 16) || !aligned(vq, 16) || !aligned(vs, 16))
     return kv_fail(FP4_EINVAL, "the cache's arrays must be 16-byte aligned");

@@ -71,9 +71,23 @@ __device__ __forceinline__ void kv_query_scale(uint32_t m, float& up, float& dow
 }
 
 // 1 / sum of weights (0 for a row that saw no key, NaN for a NaN sum), and the row's log-sum-exp.
+// Weights are exp2(z + bias), bias = kShift - maximum.
 __device__ __forceinline__ float kv_inverse(float l) { return l > 0.0f ? 1.0f / l : l; }
-__device__ __forceinline__ float kv_lse(float m, float l) {
-  return l == 0.0f ? -INFINITY : (m - kShift + log2f(l)) * 0.693147181f;
+__device__ __forceinline__ float kv_lse(float bias, float l) {
+  return l == 0.0f ? -INFINITY : (log2f(l) - bias) * 0.693147181f;
+}
+
+// Maxima are taken of the sums that the MMAs give, before their factor `c`: it has to be positive.  The
+// sign goes into the queries (`up` multiplies them), and a factor of 0 makes them zeros.
+__device__ __forceinline__ void kv_positive(float& c, float& up) {
+  if (c < 0.0f) {
+    c = -c;
+    up = -up;
+  }
+  if (c == 0.0f) {
+    c = 1.0f;
+    up = 0.0f;
+  }
 }
 
 // ---------------------------------------------------------------------------------------------

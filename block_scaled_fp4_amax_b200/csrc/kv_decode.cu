@@ -55,8 +55,8 @@ struct DecodeParams {
   uint32_t* status;
 };
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
@@ -117,45 +117,46 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   KvCursor fill, use;
   kv_seek<kTile>(a, fill, sched, seq0, nseq, x0);
   use = fill;
-  const uint32_t row_bytes = D / 2;
+  constexpr int kRow = D / 2;  // nibble bytes of a token
   const int my16 = 16 * warp;
-  long long fx = x0;
-  // page ids of this warp's next 32 tiles of the current unit, one a lane
-  int ids = -1, ids_tile = -1;
-  uint32_t absent = 0u;  // bit i: stage i holds tokens without a page (zeros)
+  int left = (int)(x1 - x0);   // tiles still to fetch
+  // Where this warp's 16 tokens of the next 32 tiles of the unit lie, one tile a lane: the cache's rows in
+  // groups of 16 (they fit 32 bits), -1 without a page.
+  int places = -1, places_tile = -1;
+  uint32_t absent = 0u;  // bit i: the tokens of stage i have no page (their bytes are some others)
+  constexpr int SL = S::kS / 16;  // lanes that copy the scales of one array
+  const uint8_t* kq_lane = a.c.kq + 16 * lane;
+  const uint8_t* vq_lane = a.c.vq + 16 * lane;
+  const uint8_t* sc_lane = lane < SL ? a.c.ks + 16 * lane : a.c.vs + 16 * (lane - SL);
+  const uint32_t ring_lane = smem_u32(ring) + 16 * lane;
 
   auto fetch = [&](int stage) {
-    if (fx >= x1) { cp_commit(); return; }
-    if (ids_tile < 0 || fill.tile - ids_tile >= 32) {
-      ids_tile = fill.tile;
-      const long long j = (long long)(fill.first + fill.tile + lane) * kTile + my16;
-      const long long pg = j >> a.c.page_shift;
-      ids = pg < a.max_pages ? __ldg(a.table + (seq0 + fill.seq) * a.table_stride + pg) : -1;
-    }
-    const int page = __shfl_sync(0xFFFFFFFFu, ids, fill.tile - ids_tile);
-    const bool live = page >= 0 && page < a.c.num_pages;
-    const int j = (fill.first + fill.tile) * kTile + my16;
-    const long long row = (((long long)(live ? page : 0) * a.c.heads + fill.head) << a.c.page_shift) +
-                          (j & ((1 << a.c.page_shift) - 1));
-    const uint32_t dst = smem_u32(ring + stage * S::kBytes);
-    const uint8_t* kq = a.c.kq + row * row_bytes;
-    const uint8_t* vq = a.c.vq + row * row_bytes;
+    if (left > 0) {
+      if (places_tile < 0 || fill.tile - places_tile >= 32) {
+        places_tile = fill.tile;
+        const int j = (fill.first + fill.tile + lane) * kTile + my16;
+        const int pg = j >> a.c.page_shift;
+        const int id = pg < a.max_pages ? __ldg(a.table + (seq0 + fill.seq) * a.table_stride + pg) : -1;
+        places = id >= 0 && id < a.c.num_pages
+                     ? ((id * a.c.heads + fill.head) << (a.c.page_shift - 4)) + ((j & ((1 << a.c.page_shift) - 1)) >> 4) : -1;
+      }
+      const int place = __shfl_sync(0xFFFFFFFFu, places, fill.tile - places_tile);
+      const uint32_t bit = 1u << stage;
+      absent = place < 0 ? absent | bit : absent & ~bit;
+      const long long at = max(place, 0);
+      const uint32_t dst = ring_lane + stage * S::kBytes;
 #pragma unroll
-    for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + 512 * i + 16 * lane, kq + 512 * i + 16 * lane, live);
+      for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + 512 * i, kq_lane + at * S::kQ + 512 * i);
 #pragma unroll
-    for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + S::kQ + 512 * i + 16 * lane, vq + 512 * i + 16 * lane, live);
-    constexpr int SL = S::kS / 16;  // lanes that copy the scales of one array
-    if (lane < 2 * SL) {
-      const uint8_t* s = (lane < SL ? a.c.ks : a.c.vs) + row * NB;
-      cp_async16(dst + 2 * S::kQ + 16 * lane, s + 16 * (lane < SL ? lane : lane - SL), live);
+      for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + S::kQ + 512 * i, vq_lane + at * S::kQ + 512 * i);
+      if (lane < 2 * SL) cp_async16(dst + 2 * S::kQ, sc_lane + at * S::kS);
+      --left;
+      if (++fill.tile == fill.tiles) {
+        kv_next<kTile>(a, fill, sched, seq0, nseq);
+        places_tile = -1;
+      }
     }
     cp_commit();
-    absent = live ? absent & ~(1u << stage) : absent | (1u << stage);
-    ++fx;
-    if (++fill.tile == fill.tiles) {
-      kv_next<kTile>(a, fill, sched, seq0, nseq);
-      ids_tile = -1;
-    }
   };
 
 #pragma unroll
@@ -194,10 +195,12 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       float up, down;
       kv_query_scale(m, up, down);
+      float c = a.scale * 1.44269504f * (NV ? __ldg(a.c.k_global) : 1.0f) * down;
+      kv_positive(c, up);
+      coef[nt] = c;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
         qf[nt][i] = f16x2_pack(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xFFFF0000u) * up);
-      coef[nt] = a.scale * 1.44269504f * (NV ? __ldg(a.c.k_global) : 1.0f) * down;
     }
     // the coefficients of this lane's score columns (rows 8 n + 2 t and 8 n + 2 t + 1)
     float cz[NT][2];
@@ -207,10 +210,12 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       cz[nt][1] = __shfl_sync(0xFFFFFFFFu, coef[nt], 8 * t + 4);
     }
 
-    float o[NT][MT][4], mx[NT][2], sum[NT][2];
+    // weights are exp2(sum * cz + bias); `raise` is the sum past which the bias changes
+    float o[NT][MT][4], bias[NT][2], raise[NT][2], sum[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
-      mx[nt][0] = mx[nt][1] = kNoMax;
+      bias[nt][0] = bias[nt][1] = -kNoMax;
+      raise[nt][0] = raise[nt][1] = kNoMax;
       sum[nt][0] = sum[nt][1] = 0.0f;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -238,7 +243,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
         uint32_t ks2[2][2];  // the scales of the thread's channels (first and second half of them), doubled
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-          const uint8_t* src = st + (tok + 8 * u) * row_bytes + t * (D / 8);
+          const uint8_t* src = st + (tok + 8 * u) * kRow + t * (D / 8);
           if constexpr (KW == 4) {
             const uint4 w = *reinterpret_cast<const uint4*>(src);
             kw[u][0] = w.x; kw[u][1] = w.y; kw[u][2] = w.z; kw[u][3] = w.w;
@@ -255,9 +260,6 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
             ks2[u][0] = ks2[u][1] = kv_scale_f16x2<NV>(sc[t * (D / 4) / B]);
           }
         }
-        float s2[NT][4];  // a second chain of sums: half the latency of one
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) s2[nt][0] = s2[nt][1] = s2[nt][2] = s2[nt][3] = 0.0f;
 #pragma unroll
         for (int w = 0; w < KW; ++w) {
           uint32_t h[2][4];
@@ -271,13 +273,9 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
           for (int i = 0; i < 2; ++i) {
             const uint32_t af[4] = {h[0][2 * i], h[1][2 * i], h[0][2 * i + 1], h[1][2 * i + 1]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(i == 0 ? s[nt] : s2[nt], af, qf[nt][4 * w + 2 * i], qf[nt][4 * w + 2 * i + 1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], af, qf[nt][4 * w + 2 * i], qf[nt][4 * w + 2 * i + 1]);
           }
         }
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int c = 0; c < 4; ++c) s[nt][c] = (s[nt][c] + s2[nt][c]) * cz[nt][c & 1];
       }
 
       // ---- mask: only where some row's range ends inside the 16 tokens, or a page is missing
@@ -295,12 +293,12 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       }
 
       // ---- running maximum (raised rarely), weights, sums
-      bool raise = false;
+      bool up = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) raise |= fmaxf(s[nt][c], s[nt][c + 2]) > mx[nt][c] + kRaise;
-      if (__any_sync(0xFFFFFFFFu, raise)) {
+        for (int c = 0; c < 2; ++c) up |= fmaxf(s[nt][c], s[nt][c + 2]) > raise[nt][c];
+      if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -308,14 +306,17 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
             float m = fmaxf(s[nt][c], s[nt][c + 2]);
 #pragma unroll
             for (int x2 = 4; x2 < 32; x2 <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x2));
-            m = fmaxf(m, mx[nt][c]);
-            const float f = exp2_approx(mx[nt][c] - m);
-            mx[nt][c] = m;
-            sum[nt][c] *= f;
+            if (m > raise[nt][c]) {  // the same for the lanes that share the row
+              raise[nt][c] = m + __fdividef(kRaise, cz[nt][c]);
+              const float to = kShift - m * cz[nt][c];
+              const float f = exp2_approx(to - bias[nt][c]);
+              bias[nt][c] = to;
+              sum[nt][c] *= f;
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-              o[nt][i][c] *= f;
-              o[nt][i][c + 2] *= f;
+              for (int i = 0; i < MT; ++i) {
+                o[nt][i][c] *= f;
+                o[nt][i][c + 2] *= f;
+              }
             }
           }
       }
@@ -325,7 +326,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
         float w[4];
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
-          w[c] = exp2_approx(s[nt][c] - (mx[nt][c & 1] - kShift));
+          w[c] = exp2_approx(__fmaf_rn(s[nt][c], cz[nt][c & 1], bias[nt][c & 1]));
           sum[nt][c & 1] += w[c];
         }
         pf[nt][0] = transpose8x8(f16x2_pack(w[0], w[1]));
@@ -339,7 +340,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
 #pragma unroll
         for (int u = 0; u < 4; ++u) {
           const int tk = ((u & 1) ? tB : tA) + (u >= 2 ? 8 : 0);
-          const uint8_t* src = st + S::kQ + tk * row_bytes + g * (D / 16);
+          const uint8_t* src = st + S::kQ + tk * kRow + g * (D / 16);
           if constexpr (VW == 2) {
             const uint2 w = *reinterpret_cast<const uint2*>(src);
             vw[u][0] = w.x; vw[u][1] = w.y;
@@ -354,16 +355,19 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
         }
 #pragma unroll
         for (int w = 0; w < VW; ++w) {
-          uint32_t h[4][4];
+          // nibbles of two tokens side by side in a byte, so that one conversion gives a fragment pair:
+          // even channels (low nibbles) and odd ones
+          uint32_t h[2][2][4];
 #pragma unroll
-          for (int u = 0; u < 4; ++u) e2m1x8_to_f16x2(vw[u][w], h[u]);
+          for (int u = 0; u < 2; ++u) {
+            const uint32_t x = vw[2 * u][w], y = vw[2 * u + 1][w];
+            e2m1x8_to_f16x2((x & 0x0F0F0F0Fu) | ((y << 4) & 0xF0F0F0F0u), h[u][0]);
+            e2m1x8_to_f16x2(((x >> 4) & 0x0F0F0F0Fu) | (y & 0xF0F0F0F0u), h[u][1]);
+          }
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
-            uint32_t af[4];
-            af[0] = f16x2_mul(__byte_perm(h[0][i], h[1][i], 0x5410), vs2[0]);
-            af[1] = f16x2_mul(__byte_perm(h[0][i], h[1][i], 0x7632), vs2[0]);
-            af[2] = f16x2_mul(__byte_perm(h[2][i], h[3][i], 0x5410), vs2[1]);
-            af[3] = f16x2_mul(__byte_perm(h[2][i], h[3][i], 0x7632), vs2[1]);
+            const uint32_t af[4] = {f16x2_mul(h[0][0][i], vs2[0]), f16x2_mul(h[0][1][i], vs2[0]),
+                                    f16x2_mul(h[1][0][i], vs2[1]), f16x2_mul(h[1][1][i], vs2[1])};
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][4 * w + i], af, pf[nt][0], pf[nt][1]);
           }
@@ -379,7 +383,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       for (int c = 0; c < 2; ++c) {
 #pragma unroll
         for (int x2 = 4; x2 < 32; x2 <<= 1) sum[nt][c] += __shfl_xor_sync(0xFFFFFFFFu, sum[nt][c], x2);
-        if (g == 0) merge_ml[warp * 8 * NT + 8 * nt + 2 * t + c] = make_float2(mx[nt][c], sum[nt][c]);
+        if (g == 0) merge_ml[warp * 8 * NT + 8 * nt + 2 * t + c] = make_float2(bias[nt][c], sum[nt][c]);
         float* dst = merge + (warp * 8 * NT + 8 * nt + 2 * t + c) * LD + 2 * g;
 #pragma unroll
         for (int i = 0; i < MT; ++i) *reinterpret_cast<float2*>(dst + 16 * i) = make_float2(o[nt][i][c], o[nt][i][c + 2]);
@@ -394,14 +398,14 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
     for (int i = threadIdx.x; i < rows * PAIRS; i += 32 * kWarps) {
       const int r = i / PAIRS, d2 = i % PAIRS;  // channels 2 d2, 2 d2 + 1
       const int at = (d2 % (D / 16)) * 16 + 2 * (d2 / (D / 16));
-      float m = kNoMax;
+      float m = -kNoMax;  // the smallest bias
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) m = fmaxf(m, merge_ml[w * 8 * NT + r].x);
+      for (int w = 0; w < kWarps; ++w) m = fminf(m, merge_ml[w * 8 * NT + r].x);
       float l = 0.0f, v0 = 0.0f, v1 = 0.0f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float2 ml = merge_ml[w * 8 * NT + r];
-        const float f = exp2_approx(ml.x - m);
+        const float f = exp2_approx(m - ml.x);
         const float2 v = *reinterpret_cast<const float2*>(merge + (w * 8 * NT + r) * LD + at);
         l += f * ml.y;
         v0 += f * v.x;
@@ -444,15 +448,15 @@ __global__ void __launch_bounds__(D) kv_decode_join_kernel(DecodeParams p, int r
   const KvSpan span = kv_span(a, join.seq);
   if (r >= span.queries * p.group) return;
   auto at = [&](int i) { return (2LL * (cta + i) + (i == 0 ? join.slot : 0)) * rows_cap + r; };
-  float m = kNoMax;
-  for (int i = threadIdx.x & 31; i < join.parts; i += 32) m = fmaxf(m, p.part_ml[at(i)].x);
+  float m = -kNoMax;
+  for (int i = threadIdx.x & 31; i < join.parts; i += 32) m = fminf(m, p.part_ml[at(i)].x);
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
+  for (int x = 16; x > 0; x >>= 1) m = fminf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
   float l = 0.0f, v = 0.0f;
 #pragma unroll 8
   for (int i = 0; i < join.parts; ++i) {
     const float2 ml = p.part_ml[at(i)];
-    const float f = exp2_approx(ml.x - m);
+    const float f = exp2_approx(m - ml.x);
     l += f * ml.y;
     v += f * p.part[at(i) * D + threadIdx.x];
   }

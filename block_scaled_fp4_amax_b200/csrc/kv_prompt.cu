@@ -179,10 +179,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         float up, down;
         kv_query_scale(top, up, down);
         coef = a.scale * 1.44269504f * (NV ? __ldg(a.c.k_global) : 1.0f) * down;
-        // the maximum is taken of the sums, so their factor must be positive: the sign goes to the
-        // queries, and a factor of 0 makes them zeros
-        if (coef < 0.0f) { coef = -coef; up = -up; }
-        if (coef == 0.0f) { coef = 1.0f; up = 0.0f; }
+        kv_positive(coef, up);
         const uint32_t q_tile = smem + L::kQ + m * L::kTile;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
@@ -306,7 +303,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
           }
         }
         if (have && p.splits == 1) {
-          if (a.lse) a.lse[out_row] = kv_lse(mx, sum);
+          if (a.lse) a.lse[out_row] = kv_lse(kShift - mx, sum);
         } else if (have) {
           p.part_ml[part_row] = make_float2(mx, sum);
         }
@@ -488,7 +485,7 @@ __global__ void __launch_bounds__(256) kv_prompt_join_kernel(PromptParams p) {
 #pragma unroll
   for (int j = 0; j < PER; j += 2)
     reinterpret_cast<uint32_t*>(a.out)[(out_row * D + lane * PER + j) / 2] = bf16x2_pack(v[j] * inv, v[j + 1] * inv);
-  if (a.lse && lane == 0) a.lse[out_row] = kv_lse(m, l);
+  if (a.lse && lane == 0) a.lse[out_row] = kv_lse(kShift - m, l);
 }
 
 template <int D, bool NV>
