@@ -36,14 +36,14 @@ constexpr int kStages = 4;
 
 // Rows a CTA handles (8 per n-tile) and CTAs per SM.
 template <int NT> struct DecodeCfg {
-  static constexpr int kCtas = NT == 1 ? 4 : (NT == 2 ? 3 : 2);
+  static constexpr int kCtas = NT == 1 ? 4 : 3;
 };
 
 constexpr int kMaxCtasPerSm = 4;
 // Rows of partial results an SM's CTAs may leave: two slots a CTA, 8 NT rows a slot.
-constexpr int kPartRowsPerSm = 2 * 2 * 32;
+constexpr int kPartRowsPerSm = 3 * 2 * 16;
 static_assert(DecodeCfg<1>::kCtas * 16 <= kPartRowsPerSm && DecodeCfg<2>::kCtas * 32 <= kPartRowsPerSm &&
-              DecodeCfg<4>::kCtas * 64 <= kPartRowsPerSm && DecodeCfg<1>::kCtas <= kMaxCtasPerSm, "workspace");
+              DecodeCfg<1>::kCtas <= kMaxCtasPerSm && kKvDecodeRows == 16, "workspace");
 
 struct DecodeParams {
   KvAttentionLaunch a;
@@ -436,35 +436,66 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   if (threadIdx.x == 0) p.joins[blockIdx.y * gridDim.x + cta] = join;
 }
 
-// Joins the parts of one unit's row: part 0 lies in the slot `join.slot` of the CTA that began the
-// unit, the others in slot 0 of the CTAs after it.
+// Joins the parts of a unit: part 0 lies in the slot `join.slot` of the CTA that began the unit, the others
+// in slot 0 of the CTAs after it (up to a whole grid of them: one long sequence).  A block takes eight
+// rows, four warps a row; each warp adds every fourth part, D / 32 channels a lane.
+constexpr int kJoinRows = 8, kJoinWays = 4;
 template <int D>
-__global__ void __launch_bounds__(D) kv_decode_join_kernel(DecodeParams p, int rows_cap) {
+__global__ void __launch_bounds__(32 * kJoinRows * kJoinWays) kv_decode_join_kernel(DecodeParams p, int rows_cap) {
+  __shared__ float part[kJoinWays][kJoinRows][D], sums[kJoinWays][kJoinRows];
   grid_dep_wait();
   const KvAttentionLaunch& a = p.a;
-  const int cta = blockIdx.x, r = blockIdx.y;
+  const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r8 = warp % kJoinRows, way = warp / kJoinRows, r = blockIdx.y * kJoinRows + r8;
   const KvJoin join = p.joins[cta];
   if (join.parts == 0) return;
   const KvSpan span = kv_span(a, join.seq);
-  if (r >= span.queries * p.group) return;
-  auto at = [&](int i) { return (2LL * (cta + i) + (i == 0 ? join.slot : 0)) * rows_cap + r; };
-  float m = -kNoMax;
-  for (int i = threadIdx.x & 31; i < join.parts; i += 32) m = fminf(m, p.part_ml[at(i)].x);
+  const bool have = r < span.queries * p.group;
+  constexpr int PER = D / 32;
+  float bias = -kNoMax;
+  if (have) {
+    const long long at0 = (2LL * cta + join.slot) * rows_cap + r, at1 = 2LL * (cta + 1) * rows_cap + r;
+    auto at = [&](int i) { return i == 0 ? at0 : at1 + 2LL * (i - 1) * rows_cap; };
+    for (int i = lane; i < join.parts; i += 32) bias = fminf(bias, p.part_ml[at(i)].x);
 #pragma unroll
-  for (int x = 16; x > 0; x >>= 1) m = fminf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x));
-  float l = 0.0f, v = 0.0f;
-#pragma unroll 8
-  for (int i = 0; i < join.parts; ++i) {
-    const float2 ml = p.part_ml[at(i)];
-    const float f = exp2_approx(m - ml.x);
-    l += f * ml.y;
-    v += f * p.part[at(i) * D + threadIdx.x];
+    for (int x = 16; x > 0; x >>= 1) bias = fminf(bias, __shfl_xor_sync(0xFFFFFFFFu, bias, x));
+    float l = 0.0f, v[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] = 0.0f;
+#pragma unroll 4
+    for (int i = way; i < join.parts; i += kJoinWays) {
+      const float2 ml = p.part_ml[at(i)];
+      const float f = exp2_approx(bias - ml.x);
+      l += f * ml.y;
+#pragma unroll
+      for (int j = 0; j < PER; j += 2) {
+        const float2 o = *reinterpret_cast<const float2*>(p.part + at(i) * D + lane * PER + j);
+        v[j] += f * o.x;
+        v[j + 1] += f * o.y;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) part[way][r8][lane * PER + j] = v[j];
+    if (lane == 0) sums[way][r8] = l;
+  }
+  __syncthreads();
+  if (!have || way != 0) return;
+  float l = 0.0f, v[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) v[j] = 0.0f;
+#pragma unroll
+  for (int w = 0; w < kJoinWays; ++w) {
+    l += sums[w][r8];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) v[j] += part[w][r8][lane * PER + j];
   }
   const int qi = r / p.group;
   const long long row = (span.first_q + qi) * a.q_heads + join.head * p.group + (r - qi * p.group);
-  const float gv = a.c.nv ? __ldg(a.c.v_global) : 1.0f;
-  reinterpret_cast<__nv_bfloat16*>(a.out)[row * D + threadIdx.x] = __float2bfloat16(v * (kv_inverse(l) * gv));
-  if (a.lse && threadIdx.x == 0) a.lse[row] = kv_lse(m, l);
+  const float inv = kv_inverse(l) * (a.c.nv ? __ldg(a.c.v_global) : 1.0f);
+#pragma unroll
+  for (int j = 0; j < PER; j += 2)
+    reinterpret_cast<uint32_t*>(a.out)[(row * D + lane * PER + j) / 2] = bf16x2_pack(v[j] * inv, v[j + 1] * inv);
+  if (a.lse && lane == 0) a.lse[row] = kv_lse(bias, l);
 }
 
 template <int D, bool NV, int NT>
@@ -486,15 +517,15 @@ cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
   kv_decode_kernel<D, NV, NT><<<dim3(n, chunks), 32 * kWarps, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
   const int rows = min(p.a.max_q * p.group, 8 * NT);
-  return launch_pdl(kv_decode_join_kernel<D>, dim3(n * chunks, rows), dim3(D), 0, s, true, p, 8 * NT);
+  return launch_pdl(kv_decode_join_kernel<D>, dim3(n * chunks, (rows + kJoinRows - 1) / kJoinRows),
+                    dim3(32 * kJoinRows * kJoinWays), 0, s, true, p, 8 * NT);
 }
 
 template <int D, bool NV>
 cudaError_t decode_rows(DecodeParams& p, cudaStream_t s) {
   const int rows = p.a.max_q * p.group;
   if (rows <= 8) return decode_t<D, NV, 1>(p, s);
-  if (rows <= 16) return decode_t<D, NV, 2>(p, s);
-  return decode_t<D, NV, 4>(p, s);
+  return decode_t<D, NV, 2>(p, s);
 }
 
 }  // namespace
