@@ -68,6 +68,13 @@ __device__ __forceinline__ f32x2 f2_fma(f32x2 a, f32x2 b, f32x2 c) {
   return d;
 }
 
+// Largest of three; a NaN operand is passed over.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float r;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // kind::f16, fp32 accumulator, f16 operands, M = 128; B N-major (bit 16) for the values.
 __host__ __device__ constexpr uint32_t idesc_prompt(int n, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
@@ -198,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       const uint32_t t_s = tmem + 128 * m + ((uint32_t)((warp & 3) * 32) << 16);
       const uint32_t t_o = tmem + 256 + D * m + ((uint32_t)((warp & 3) * 32) << 16);
       float mx = kNoMax;
-      f32x2 sum2 = 0ull;
+      f32x2 sums[4] = {0ull, 0ull, 0ull, 0ull};
       bool ok = true;
       for (int k = 0; k < n; ++k) {
         if (!warp_wait(s_full + 8 * m, k & 1, abort_flag, p.status, 0, p.wait_ns)) { ok = false; break; }
@@ -221,16 +228,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
             if (j < l || j >= h || !page) s[j] = 0xFF800000u;  // -inf
           }
         }
-        float top = -INFINITY;
+        // eight chains of three-operand maxima
+        float t8[8];
 #pragma unroll
-        for (int j = 0; j < 128; ++j) top = fmaxf(top, __uint_as_float(s[j]));
-        top *= coef;
+        for (int j = 0; j < 8; ++j) t8[j] = __uint_as_float(s[j]);
+#pragma unroll
+        for (int i = 8; i < 120; i += 16)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) t8[j] = max3(t8[j], __uint_as_float(s[i + 2 * j]), __uint_as_float(s[i + 2 * j + 1]));
+#pragma unroll
+        for (int j = 0; j < 8; ++j) t8[j] = fmaxf(t8[j], __uint_as_float(s[120 + j]));
+        const float top = coef * max3(max3(t8[0], t8[1], t8[2]), max3(t8[3], t8[4], t8[5]), fmaxf(t8[6], t8[7]));
         const bool raise = top > mx + kRaise;
         if (__any_sync(0xFFFFFFFFu, raise)) {
           const float to = raise ? top : mx;
           const float f = exp2_approx(mx - to);
           mx = to;
-          sum2 = f2_mul(sum2, f2_pack(f, f));
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sums[j] = f2_mul(sums[j], f2_pack(f, f));
           if (k > 0) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
@@ -256,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
             f2_unpack(f2_fma(f2_pack(__uint_as_float(s[64 * h + 2 * j]), __uint_as_float(s[64 * h + 2 * j + 1])), c2, b2), x, y);
             x = exp2_approx(x);
             y = exp2_approx(y);
-            sum2 = f2_add(sum2, f2_pack(x, y));
+            sums[j & 3] = f2_add(sums[j & 3], f2_pack(x, y));
             w[j] = f16x2_pack(x, y);
           }
           TC_ST32(t_s + 32 * h, w);
@@ -269,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       tc_fence_after();
       if (ok) {
         float s0, s1;
-        f2_unpack(sum2, s0, s1);
+        f2_unpack(f2_add(f2_add(sums[0], sums[1]), f2_add(sums[2], sums[3])), s0, s1);
         const float sum = s0 + s1;
         const float inv = kv_inverse(sum) * (NV ? __ldg(a.c.v_global) : 1.0f);
         const long long out_row = (span.first_q + qi) * a.q_heads + hq;
