@@ -400,11 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
   } else {
     regs_dec<48>();
     if (warp == 12) {
-      // ---------------------------------------------------------------- MMA issuer (lane 0 issues)
+      // ---------------------------------------------------------------- MMA issuer (one elected lane)
+      const bool lead = elect_one();
       const uint32_t i_s = idesc_prompt(kKeys, false), i_o = idesc_prompt(D, true);
       bool ok = n > 0;
       auto scores = [&](int m, int k) {
-        if (lane == 0) {
+        if (lead) {
           const uint32_t q = smem + L::kQ + m * L::kTile, kt = smem + L::kK + (k & 1) * L::kTile;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
@@ -419,7 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       if (ok) {
         tc_fence_after();
         for (int m = 0; m < mtiles; ++m) scores(m, 0);
-        if (lane == 0) tc_commit(k_empty);
+        if (lead) tc_commit(k_empty);
       }
       for (int k = 0; k < n && ok; ++k) {
         const int st = k & 1;
@@ -428,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         for (int m = 0; m < mtiles; ++m) {
           if (!mbar_wait(p_ready + 8 * m, k & 1, abort_flag, p.status, 7, p.wait_ns)) { ok = false; break; }
           tc_fence_after();
-          if (lane == 0) {
+          if (lead) {
             const uint32_t vt = smem + L::kV + st * L::kTile;
 #pragma unroll
             for (int i = 0; i < kKeys / 16; ++i)
@@ -437,13 +438,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
           if (k + 1 < n) scores(m, k + 1);
         }
         if (!ok) break;
-        if (lane == 0) {
+        if (lead) {
           tc_commit(v_empty + 8 * st);
           if (k + 1 < n) tc_commit(k_empty + 8 * (st ^ 1));
           else tc_commit(o_full);
         }
       }
-      if (lane == 0) {
+      if (lead) {
         // on every path: no MMA is in flight when tensor memory is freed
         tc_commit(drain);
         mbar_drain(drain, 0);

@@ -116,6 +116,14 @@ __device__ __forceinline__ uint64_t desc_sw128_mn(uint32_t saddr, uint32_t lbo) 
          (2ull << 61);
 }
 
+// True in one lane of a converged warp.  Under this predicate an MMA takes 11 cycles to issue; under
+// `lane == 0` it took 51 (128 x 16 x 16 MMAs back to back), too slow to queue work behind a 64-cycle one.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // kind::f16 with the A operand in tensor memory (two fp16 values of a row per 32-bit column).
 __device__ __forceinline__ void tc_mma_f16_ts(uint32_t d, uint32_t a, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
