@@ -18,12 +18,14 @@ into them, fp4_kv_read brings tokens back, fp4_kv_attention attends over them.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libfp4mx.so")
+KV_BINDING_PATH = os.path.join(_HERE, "_kv_binding.so")
 
 # enums of include/fp4mx.h
 F32, BF16 = 0, 1
@@ -345,88 +347,26 @@ def fp4_kv_alloc(num_pages: int, heads: int, page_size: int, head_dim: int, fmt:
     return tuple(torch.zeros(shape + (n,), dtype=torch.uint8, device=device) for n in (half, nb, half, nb))
 
 
-# A decode step calls these once a layer, so the checks are written for few attribute reads.
+# A decoding step calls these once a layer, so their checks and marshalling are native (_kv_binding.so);
+# the functions below give them their names and defaults.
 
-def _kv_fail(name, t, want):
-    got = "None" if t is None else f"{t.dtype} {list(t.shape)} (strides {list(t.stride())}) on {t.device}"
-    raise ValueError(f"{name}: expected {want}, got {got}")
-
-
-def _kv_ints(name, t, dtype, n, dev):
-    """A contiguous integer vector of n elements on CUDA device `dev`: its address."""
-    if t.dtype is not dtype or t.dim() != 1 or t.shape[0] != n or t.get_device() != dev or not t.is_contiguous():
-        _kv_fail(name, t, f"a contiguous {dtype} tensor [{n}] on cuda:{dev}")
-    return t.data_ptr()
+_kv = None
 
 
-def _kv_cache(cache, fmt, k_global, v_global):
-    """The cache's part of the argument lists (arrays and sizes; format and scales), and its device."""
-    kq, ks, vq, vs = cache
-    if kq.dim() != 4 or not kq.is_cuda:
-        _kv_fail("kq", kq, "a CUDA tensor [pages, heads, page, head_dim / 2]")
-    shape = kq.shape
-    dev = kq.get_device()
-    pages, heads, page, half = shape
-    block = 32 if fmt == MXFP4 else 16
-    scales = (pages, heads, page, 2 * half // block)
-    if vq.shape != shape or ks.shape != scales or vs.shape != scales:
-        raise ValueError(f"cache: expected vq {list(shape)}, ks and vs {list(scales)} beside kq {list(shape)}, got "
-                         f"{list(vq.shape)}, {list(ks.shape)}, {list(vs.shape)}")
-    for t in cache:
-        if t.dtype is not torch.uint8 or not t.is_contiguous() or t.get_device() != dev:
-            _kv_fail("cache", t, f"contiguous uint8 tensors on cuda:{dev}")
-    gk = gv = None
-    if k_global is not None and v_global is not None:
-        for t in (k_global, v_global):
-            if t.dtype is not torch.float32 or t.numel() != 1 or t.get_device() != dev:
-                _kv_fail("k_global, v_global", t, f"float32 tensors of one element on cuda:{dev}")
-        gk, gv = k_global.data_ptr(), v_global.data_ptr()
-    return ((kq.data_ptr(), ks.data_ptr(), vq.data_ptr(), vs.data_ptr(), pages, page, heads, 2 * half),
-            (fmt, block, gk, gv), dev)
+def _kv_native():
+    """Load _kv_binding.so (raises if it is not built)."""
+    global _kv
+    lib()
+    if not os.path.exists(KV_BINDING_PATH):
+        raise ImportError(f"{KV_BINDING_PATH} is not built; run `python -m block_scaled_fp4_amax_b200.build`")
+    spec = importlib.util.spec_from_file_location("_kv_binding", KV_BINDING_PATH)
+    _kv = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(_kv)
+    return _kv
 
 
-def _kv_table(table, seqs, dev):
-    shape = table.shape
-    if table.dtype is not torch.int32 or len(shape) != 2 or shape[0] != seqs or table.get_device() != dev \
-            or (shape[1] > 1 and table.stride(1) != 1):
-        _kv_fail("block table", table, f"an int32 tensor [{seqs}, pages] with adjacent entries on cuda:{dev}")
-    return table.data_ptr(), (table.stride(0) if seqs > 1 else shape[1]), shape[1], seqs
-
-
-def _kv_rows(name, t, shape, dev, dtype=None):
-    """[tokens, heads, head_dim] with adjacent channels: token and head strides (an extent of one has
-    none that matters)."""
-    if t.shape != shape or t.get_device() != dev or (dtype is not None and t.dtype is not dtype):
-        _kv_fail(name, t, f"{list(shape)}{'' if dtype is None else f' {dtype}'} on cuda:{dev}")
-    st = t.stride()
-    if st[2] != 1 and t.numel():
-        raise ValueError(f"{name}: the channels must be adjacent")
-    return (st[0] if shape[0] > 1 else 0), (st[1] if shape[1] > 1 else 0)
-
-
-class _kv_on:
-    """The call's device and stream (torch's current one there by default) made current, where they are
-    not already: tensors allocated inside belong to that stream.  Gives the stream's handle."""
-    __slots__ = ("dev", "stream", "inner")
-
-    def __init__(self, dev, stream):
-        self.dev, self.stream, self.inner = dev, stream, None
-
-    def __enter__(self):
-        if self.stream is None:
-            if torch.cuda.current_device() == self.dev:
-                return torch._C._cuda_getCurrentRawStream(self.dev)
-            self.stream = torch.cuda.current_stream(self.dev)
-        self.inner = torch.cuda.stream(self.stream)
-        self.inner.__enter__()
-        if torch.cuda.current_device() != self.dev:
-            self.inner.__exit__(None, None, None)
-            raise ValueError(f"the stream belongs to another device than the cache (cuda:{self.dev})")
-        return self.stream.cuda_stream
-
-    def __exit__(self, *exc):
-        if self.inner is not None:
-            self.inner.__exit__(*exc)
+def _kv_stream(stream):
+    return None if stream is None else (stream.stream_id, stream.device_index, stream.device_type)
 
 
 def fp4_kv_append(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, fmt: int = NVFP4,
@@ -436,13 +376,7 @@ def fp4_kv_append(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, 
     k, v: bf16 or fp32 [tokens, heads, head_dim], any token and head strides (slices of a fused
     projection); slots: int64 [tokens], page * page_size + offset, negative to skip a row; k_global,
     v_global: the fixed NVFP4 scales, amax / (6 * 448), or amax / (6 * 256) with four_six."""
-    arrays, form, dev = _kv_cache(cache, fmt, k_global, v_global)
-    shape = (k.shape[0], arrays[6], arrays[7])
-    strides = _kv_rows("k", k, shape, dev) + _kv_rows("v", v, shape, dev, k.dtype)
-    at = _kv_ints("slots", slots, torch.int64, shape[0], dev)
-    with _kv_on(dev, stream) as s:
-        _check(lib().fp4_kv_append(k.data_ptr(), v.data_ptr(), _dtype_code(k), shape[0], *strides, at, form[0], form[1],
-                                   _nv_mode(four_six, False), form[2], form[3], *arrays, s))
+    _check((_kv or _kv_native()).kv_append(k, v, *cache, slots, fmt, 1 if four_six else 0, k_global, v_global, _kv_stream(stream)))
 
 
 def fp4_kv_read(cache, table: torch.Tensor, cu: torch.Tensor, total: int, fmt: int = NVFP4,
@@ -452,22 +386,15 @@ def fp4_kv_read(cache, table: torch.Tensor, cu: torch.Tensor, total: int, fmt: i
     without `starts`) of sequence b.  cu: int32 [seqs + 1]; total: rows of the outputs, cu[-1] for
     the caller that knows it.  Returns (k, v) [total, heads, head_dim] in out_dtype, or fills
     `out` = (k, v) (rows from cu[-1] on are left as they were)."""
-    arrays, form, dev = _kv_cache(cache, fmt, k_global, v_global)
-    seqs = cu.shape[0] - 1
-    rows = _kv_ints("cu", cu, torch.int32, seqs + 1, dev)
-    first = None if starts is None else _kv_ints("starts", starts, torch.int32, seqs, dev)
-    where = _kv_table(table, seqs, dev)
-    shape = (total, arrays[6], arrays[7])
-    with _kv_on(dev, stream) as s:
-        if out is None:
-            k, v = (torch.empty(shape, dtype=out_dtype, device=table.device) for _ in range(2))
-        else:
-            k, v = out
-            for t in out:
-                if t.shape != shape or t.dtype is not k.dtype or t.get_device() != dev or not t.is_contiguous():
-                    _kv_fail("out", t, f"two contiguous tensors {list(shape)} of one dtype on cuda:{dev}")
-        _check(lib().fp4_kv_read(*arrays, *form, *where, rows, first, total, _dtype_code(k), k.data_ptr(), v.data_ptr(), s))
-    return k, v
+    if out is None:
+        out = (None, None)
+        if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
+            raise TypeError(f"out_dtype must be float32 or bfloat16, got {out_dtype}")
+    r = (_kv or _kv_native()).kv_read(*cache, table, cu, total, fmt, starts, out_dtype is torch.bfloat16, k_global, v_global, *out,
+                                      _kv_stream(stream))
+    if type(r) is int:
+        _check(r)
+    return r
 
 
 def fp4_kv_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor, fmt: int = NVFP4,
@@ -482,29 +409,8 @@ def fp4_kv_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Te
     sequence); scale: 1 / sqrt(head_dim) by default; window: keys a query sees, itself the last one (0:
     all).  Returns (out bf16 [total_q, q_heads, head_dim], lse float32 [total_q, q_heads] or None);
     a query that sees no key gives zeros and lse = -inf."""
-    arrays, form, dev = _kv_cache(cache, fmt, k_global, v_global)
-    shape = q.shape
-    if len(shape) != 3 or shape[2] != arrays[7]:
-        _kv_fail("q", q, f"[tokens, query heads, {arrays[7]}]")
-    strides = _kv_rows("q", q, shape, dev)
-    total, q_heads, dim = shape
-    seqs = lens.shape[0]
-    n = _kv_ints("lens", lens, torch.int32, seqs, dev)
-    first = None if cu_q is None else _kv_ints("cu_q", cu_q, torch.int32, seqs + 1, dev)
-    where = _kv_table(table, seqs, dev)
-    L = lib()
-    with _kv_on(dev, stream) as s:
-        if out is None:
-            out = torch.empty(shape, dtype=torch.bfloat16, device=q.device)
-        elif out.shape != shape or out.dtype is not torch.bfloat16 or out.get_device() != dev or not out.is_contiguous():
-            _kv_fail("out", out, f"a contiguous bfloat16 tensor {list(shape)} on cuda:{dev}")
-        lse = torch.empty(shape[:2], dtype=torch.float32, device=q.device) if want_lse else None
-        if workspace is None:
-            workspace = torch.empty(L.fp4_workspace_size(OP_KV_ATTENTION, total, q_heads), dtype=torch.uint8, device=q.device)
-        elif workspace.get_device() != dev or not workspace.is_contiguous():
-            _kv_fail("workspace", workspace, f"a contiguous tensor on cuda:{dev}")
-        _check(L.fp4_kv_attention(q.data_ptr(), _dtype_code(q), total, *strides, q_heads, *arrays, *form, *where, first, max_q,
-                                  n, dim ** -0.5 if scale is None else scale, causal, window, out.data_ptr(),
-                                  None if lse is None else lse.data_ptr(), workspace.data_ptr(),
-                                  workspace.numel() * workspace.element_size(), s))
-    return out, lse
+    r = (_kv or _kv_native()).kv_attention(q, *cache, table, lens, fmt, cu_q, max_q, q.shape[-1] ** -0.5 if scale is None else scale,
+                                           causal, window, want_lse, k_global, v_global, out, workspace, _kv_stream(stream))
+    if type(r) is int:
+        _check(r)
+    return r

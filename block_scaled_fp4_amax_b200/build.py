@@ -3,7 +3,9 @@
     python -m block_scaled_fp4_amax_b200.build [--force]
 
 Each .cu file under csrc/ is compiled to an object in _build/ (in parallel), then linked into
-block_scaled_fp4_amax_b200/libfp4mx.so with the CUDA runtime linked statically.  The driver API
+block_scaled_fp4_amax_b200/libfp4mx.so with the CUDA runtime linked statically.  kv_binding.cpp (the
+Python binding of the key/value cache's calls, against torch's C++ headers) becomes _kv_binding.so
+beside it.  The driver API
 entry point needed for tensor maps is fetched at run time, so nothing links against libcuda.
 """
 from __future__ import annotations
@@ -21,6 +23,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libfp4mx.so")
+BINDING = os.path.join(PKG, "_kv_binding.so")
+BINDING_SRC = os.path.join(CSRC, "kv_binding.cpp")
 INCLUDE = os.path.join(ROOT, "include")
 
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
@@ -41,13 +45,13 @@ def _sources():
 
 def _deps():
     return _sources() + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(CSRC, "*.h")) + \
-        glob.glob(os.path.join(INCLUDE, "*.h")) + [os.path.abspath(__file__)]
+        glob.glob(os.path.join(INCLUDE, "*.h")) + [BINDING_SRC, os.path.abspath(__file__)]
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(BINDING):
         return False
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(BINDING))
     return all(os.path.getmtime(d) <= t for d in _deps())
 
 
@@ -62,20 +66,63 @@ def _compile(src: str, extra: list[str]) -> str:
     return obj
 
 
+def _cxx() -> str:
+    for cand in ("/usr/bin/g++", shutil.which("g++"), os.environ.get("CXX")):
+        if cand and os.path.exists(cand):
+            return cand
+    raise RuntimeError("g++ not found")
+
+
+def _compile_binding() -> str:
+    import sysconfig
+
+    import torch
+
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc())), "include")
+    obj = os.path.join(BUILD, "kv_binding.o")
+    cmd = [_cxx(), "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", "-I", inc,
+           "-I", os.path.join(inc, "torch", "csrc", "api", "include"), "-I", cuda, "-I", sysconfig.get_paths()["include"],
+           "-c", BINDING_SRC, "-o", obj]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed on {BINDING_SRC}:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    """Against libfp4mx.so beside it, and torch's libraries (loaded already when it is imported)."""
+    import torch
+
+    libs = os.path.join(os.path.dirname(torch.__file__), "lib")
+    tmp = BINDING + ".tmp"
+    # the shared libstdc++ by name: torch's exceptions cross into the binding, so both must use one copy
+    cmd = [_cxx(), "-shared", "-o", tmp, obj, "-L", PKG, "-lfp4mx", "-L", libs, "-ltorch_python", "-ltorch", "-ltorch_cpu",
+           "-lc10_cuda", "-lc10", "-l:libstdc++.so.6", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, BINDING)
+
+
 def build(force: bool = False, verbose_ptxas: bool = False) -> str:
-    """Compile every CUDA source and link libfp4mx.so; returns its path."""
+    """Compile every CUDA source and link libfp4mx.so and the binding; returns the library's path."""
     if not force and up_to_date():
         return LIB
     os.makedirs(BUILD, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
     with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(lambda s: _compile(s, extra), _sources()))
+        binding_obj = binding.result()
     tmp = LIB + ".tmp"
     cmd = [nvcc(), *ARCH, "-shared", "-cudart", "static", "-o", tmp, *objs]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{' '.join(cmd)}\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
+    _link_binding(binding_obj)
     return LIB
 
 
