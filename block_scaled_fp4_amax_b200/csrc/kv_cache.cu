@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_append_kernel(AppendParams p) {
   const long long slot = in ? p.slots[token] : -1;
   const bool live = slot >= 0 && (slot >> p.c.page_shift) < p.c.num_pages;
   Chunk16<T> x;
-  if (live) {
+  if (in) {  // whether the row is skipped or not: the loads need not wait for its slot
     const char* src = values ? p.v + token * p.v_stride + head * p.v_head_stride
                              : p.k + token * p.k_stride + head * p.k_head_stride;
     x.load(src + part * (16u * sizeof(T)));
@@ -153,24 +153,34 @@ struct ReadParams {
   void *k_out, *v_out;
 };
 
-constexpr int kReadRows = 64;  // most rows of one CTA
+constexpr int kReadRows = 64;   // most rows of one CTA
+constexpr int kReadUnroll = 4;  // chunks in flight a lane
+constexpr int kReadSeqs = 1024; // sequences whose row offsets a CTA holds
 
-// The CTA's rows are located first (binary search in cu, then the block table, one row a lane); then
-// all lanes stream the rows' chunks, keys and values.
+// The CTA's rows are located first, one row a lane (binary search in cu, copied to shared memory so that
+// its steps are not as many trips to L2, then the block table); then all lanes stream the rows'
+// chunks, keys and values.
 template <bool NV, bool OUT_BF16>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(ReadParams p) {
   __shared__ long long base[kReadRows];  // (page * heads << page_shift) + offset; -1: no page, -2: not a row
+  __shared__ int cu_near[kReadSeqs + 1];
   const long long row0 = (long long)blockIdx.x * p.rows_per_cta;
+  const bool near = p.seqs <= kReadSeqs;
+  if (near)
+    for (int i = threadIdx.x; i <= p.seqs; i += kKvThreads) cu_near[i] = __ldg(p.cu + i);
+  const float gk = NV ? *p.c.k_global : 1.0f, gv = NV ? *p.c.v_global : 1.0f;
+  const int* cu = near ? cu_near : p.cu;
+  __syncthreads();
   if (threadIdx.x < p.rows_per_cta) {
     const long long r = row0 + threadIdx.x;
     long long b = -2;
-    if (r < p.total && r < p.cu[p.seqs]) {
+    if (r < p.total && r < cu[p.seqs]) {
       int lo = 0, hi = p.seqs;  // cu[lo] <= r < cu[hi]
       while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
-        if (p.cu[mid] <= r) lo = mid; else hi = mid;
+        if (cu[mid] <= r) lo = mid; else hi = mid;
       }
-      const long long t = r - p.cu[lo] + (p.starts ? p.starts[lo] : 0);
+      const long long t = r - cu[lo] + (p.starts ? p.starts[lo] : 0);
       const long long at = t >> p.c.page_shift;
       long long page = -1;
       if (t >= 0 && at < p.max_pages) page = p.table[lo * p.table_stride + at];
@@ -180,53 +190,67 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(ReadParams p) {
     base[threadIdx.x] = b;
   }
   __syncthreads();
-  const float gk = NV ? *p.c.k_global : 1.0f, gv = NV ? *p.c.v_global : 1.0f;
   const uint32_t per_row = (uint32_t)p.c.head_dim / 16u;
   const uint32_t shift = per_row == 8u ? 3u : 2u;
   const uint32_t n = (uint32_t)p.rows_per_cta * p.per_token.d;  // chunks of keys; as many of values follow
-  for (uint32_t i = threadIdx.x; i < 2 * n; i += kKvThreads) {
-    const bool values = i >= n;
-    const uint32_t c = values ? i - n : i;
-    const uint32_t r = div_u32(c, p.per_token);
-    const uint32_t rest = c - r * p.per_token.d;
-    const long long b = base[r];
-    if (b == -2) continue;
-    const uint32_t head = rest >> shift, part = rest & (per_row - 1u);
-    const long long row = b + ((long long)head << p.c.page_shift);
-    uint2 w = make_uint2(0u, 0u);
-    uint32_t sb = NV ? 0u : 127u;
-    if (b >= 0) {
-      w = __ldg(reinterpret_cast<const uint2*>(values ? p.c.vq : p.c.kq) + row * per_row + part);
-      const uint8_t* s = values ? p.c.vs : p.c.ks;
-      sb = NV ? __ldg(s + row * per_row + part) : __ldg(s + row * (per_row / 2) + part / 2);
+  for (uint32_t i0 = threadIdx.x; i0 < 2 * n; i0 += kReadUnroll * kKvThreads) {
+    uint2 words[kReadUnroll];
+    uint32_t bytes[kReadUnroll], rows[kReadUnroll], rests[kReadUnroll];
+#pragma unroll
+    for (int j = 0; j < kReadUnroll; ++j) {
+      const uint32_t i = i0 + j * kKvThreads;
+      const bool values = i >= n;
+      const uint32_t c = values ? i - n : i;
+      const uint32_t r = div_u32(c, p.per_token);
+      const uint32_t rest = c - r * p.per_token.d;
+      rows[j] = r;
+      rests[j] = rest;
+      words[j] = make_uint2(0u, 0u);
+      bytes[j] = NV ? 0u : 127u;
+      const long long b = i < 2 * n ? base[r] : -2;
+      if (b >= 0) {
+        const uint32_t part = rest & (per_row - 1u);
+        const long long row = b + ((long long)(rest >> shift) << p.c.page_shift);
+        words[j] = __ldg(reinterpret_cast<const uint2*>(values ? p.c.vq : p.c.kq) + row * per_row + part);
+        const uint8_t* sc = values ? p.c.vs : p.c.ks;
+        bytes[j] = NV ? __ldg(sc + row * per_row + part) : __ldg(sc + row * (per_row / 2) + part / 2);
+      }
     }
-    float v[16], o[16];
-    e2m1_unpack<8>(w.x, v);
-    e2m1_unpack<8>(w.y, v + 8);
-    if (NV) {
-      const float d = e4m3_value(sb), g = values ? gv : gk;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] = __fmul_rn(__fmul_rn(v[j], d), g);
-    } else {
-      // 2^(sb - 127), byte 0 (2^-127, subnormal) as two exact factors; byte 255 as fp4_dequantize
-      const float d0 = sb != 0u ? __uint_as_float(sb << 23) : 0x1p-64f, d1 = sb != 0u ? 1.0f : 0x1p-63f;
+    for (int j = 0; j < kReadUnroll; ++j) {
+      const uint32_t i = i0 + j * kKvThreads;
+      if (i >= 2 * n || base[rows[j]] == -2) continue;
+      const bool values = i >= n;
+      const uint32_t r = rows[j], head = rests[j] >> shift, part = rests[j] & (per_row - 1u), sb = bytes[j];
+      const uint2 w = words[j];
+      float v[16], o[16];
+      e2m1_unpack<8>(w.x, v);
+      e2m1_unpack<8>(w.y, v + 8);
+      if (NV) {
+        const float d = e4m3_value(sb), g = values ? gv : gk;
 #pragma unroll
-      for (int j = 0; j < 16; ++j) o[j] = __fmul_rn(__fmul_rn(v[j], d0), d1);
-    }
-    const long long at = ((row0 + r) * p.c.heads + head) * p.c.head_dim + part * 16u;
-    void* out = values ? p.v_out : p.k_out;
-    if (OUT_BF16) {
-      uint32_t pw[8];
+        for (int x = 0; x < 16; ++x) o[x] = __fmul_rn(__fmul_rn(v[x], d), g);
+      } else {
+        // 2^(sb - 127), byte 0 (2^-127, subnormal) as two exact factors; byte 255 as fp4_dequantize
+        const float d0 = sb != 0u ? __uint_as_float(sb << 23) : 0x1p-64f, d1 = sb != 0u ? 1.0f : 0x1p-63f;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) pw[j] = bf16x2_pack(o[2 * j], o[2 * j + 1]);
-      st32(reinterpret_cast<__nv_bfloat16*>(out) + at, pw);
-    } else {
+        for (int x = 0; x < 16; ++x) o[x] = __fmul_rn(__fmul_rn(v[x], d0), d1);
+      }
+      const long long at = ((row0 + r) * p.c.heads + head) * p.c.head_dim + part * 16u;
+      void* out = values ? p.v_out : p.k_out;
+      if (OUT_BF16) {
+        uint32_t pw[8];
 #pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        uint32_t w8[8];
+        for (int x = 0; x < 8; ++x) pw[x] = bf16x2_pack(o[2 * x], o[2 * x + 1]);
+        st32(reinterpret_cast<__nv_bfloat16*>(out) + at, pw);
+      } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) w8[j] = __float_as_uint(o[8 * h + j]);
-        st32(reinterpret_cast<float*>(out) + at + 8 * h, w8);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t w8[8];
+#pragma unroll
+          for (int x = 0; x < 8; ++x) w8[x] = __float_as_uint(o[8 * h + x]);
+          st32(reinterpret_cast<float*>(out) + at + 8 * h, w8);
+        }
       }
     }
   }
@@ -263,9 +287,11 @@ cudaError_t launch_kv_read(const KvReadLaunch& L, cudaStream_t s) {
   p.cu = L.cu;
   p.total = L.total;
   const int per_token = L.c.heads * (L.c.head_dim / 16);
-  p.rows_per_cta = 8 * kKvThreads / (2 * per_token);  // eight chunks a lane
-  if (p.rows_per_cta < 1) p.rows_per_cta = 1;
-  if (p.rows_per_cta > kReadRows) p.rows_per_cta = kReadRows;
+  // Eight chunks a lane, fewer where that would leave SMs without a CTA (517 rows of 8 heads: 16 -> 2 rows).
+  long long rows = 8 * kKvThreads / (2 * per_token);
+  const long long spread = (L.total + 2 * num_sms() - 1) / (2 * num_sms());
+  if (rows > spread) rows = spread;
+  p.rows_per_cta = (int)(rows < 1 ? 1 : (rows > kReadRows ? kReadRows : rows));
   p.per_token = make_divu32((uint32_t)per_token);
   p.k_out = L.k_out;
   p.v_out = L.v_out;

@@ -3,12 +3,12 @@
 //
 // The cache is read once, so the work is bound by its bytes (144 a token and head at head_dim 128)
 // as long as unpacking keeps up: 1.5 instructions a value.  A unit of work is one (sequence, head).
-// All units' tiles of 64 tokens are laid end to end, and CTA i of n takes tiles [i T / n, (i + 1) T / n),
+// All units' tiles of 128 tokens are laid end to end, and CTA i of n takes tiles [i T / n, (i + 1) T / n),
 // whatever the lengths (which only the device knows), so every CTA has the same number of tiles; a
 // unit that falls into several CTAs is written as fp32 partial results that a second, small launch
 // joins (launched programmatically: it is resident when the first one drains).
 //
-// Inside a CTA each of the four warps takes 16 tokens of a tile and keeps its own running maximum,
+// Inside a CTA each of the four warps takes 32 tokens of a tile and keeps its own running maximum,
 // sum and output; they meet once at the end of a unit.  Bytes come through a ring of cp.async
 // stages per warp (no CTA barrier in the loop) and are expanded in registers, straight into the
 // fragments of mma.m16n8k16 (f16 x f16 + f32):
@@ -31,8 +31,11 @@ namespace fp4k {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kTile = 16 * kWarps;  // tokens of a CTA step
-constexpr int kStages = 4;
+// A warp's step: 32 tokens as two groups of 16 (with one group the bookkeeping around it, a third of the
+// instructions, was the largest single part of a step).
+constexpr int kGroups = 2, kWarpTokens = 16 * kGroups;
+constexpr int kTile = kWarpTokens * kWarps;  // tokens of a CTA step
+constexpr int kStages = 2;
 
 // Rows a CTA handles (8 per n-tile) and CTAs per SM.
 template <int NT> struct DecodeCfg {
@@ -77,7 +80,8 @@ struct StageCfg {
   static constexpr int B = NV ? 16 : 32;
   static constexpr int kQ = 16 * D / 2;   // nibble bytes of 16 tokens
   static constexpr int kS = 16 * (D / B); // scale bytes
-  static constexpr int kBytes = 2 * kQ + 2 * kS;
+  static constexpr int kGroup = 2 * kQ + 2 * kS;
+  static constexpr int kBytes = kGroups * kGroup;
 };
 
 template <int D, bool NV, int NT>
@@ -118,12 +122,12 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   kv_seek<kTile>(a, fill, sched, seq0, nseq, x0);
   use = fill;
   constexpr int kRow = D / 2;  // nibble bytes of a token
-  const int my16 = 16 * warp;
+  const int mine = kWarpTokens * warp;  // of a tile's tokens
   int left = (int)(x1 - x0);   // tiles still to fetch
-  // Where this warp's 16 tokens of the next 32 tiles of the unit lie, one tile a lane: the cache's rows in
+  // Where this warp's groups of the next 16 tiles of the unit lie, one group a lane: the cache's rows in
   // groups of 16 (they fit 32 bits), -1 without a page.
   int places = -1, places_tile = -1;
-  uint32_t absent = 0u;  // bit i: the tokens of stage i have no page (their bytes are some others)
+  uint32_t absent = 0u;  // bit 2 i + h: group h of stage i has no page (its bytes are some others)
   constexpr int SL = S::kS / 16;  // lanes that copy the scales of one array
   const uint8_t* kq_lane = a.c.kq + 16 * lane;
   const uint8_t* vq_lane = a.c.vq + 16 * lane;
@@ -132,24 +136,27 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
 
   auto fetch = [&](int stage) {
     if (left > 0) {
-      if (places_tile < 0 || fill.tile - places_tile >= 32) {
+      if (places_tile < 0 || fill.tile - places_tile >= 32 / kGroups) {
         places_tile = fill.tile;
-        const int j = (fill.first + fill.tile + lane) * kTile + my16;
+        const int j = (fill.first + fill.tile + lane / kGroups) * kTile + mine + 16 * (lane % kGroups);
         const int pg = j >> a.c.page_shift;
         const int id = pg < a.max_pages ? __ldg(a.table + (seq0 + fill.seq) * a.table_stride + pg) : -1;
         places = id >= 0 && id < a.c.num_pages
                      ? ((id * a.c.heads + fill.head) << (a.c.page_shift - 4)) + ((j & ((1 << a.c.page_shift) - 1)) >> 4) : -1;
       }
-      const int place = __shfl_sync(0xFFFFFFFFu, places, fill.tile - places_tile);
-      const uint32_t bit = 1u << stage;
-      absent = place < 0 ? absent | bit : absent & ~bit;
-      const long long at = max(place, 0);
-      const uint32_t dst = ring_lane + stage * S::kBytes;
 #pragma unroll
-      for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + 512 * i, kq_lane + at * S::kQ + 512 * i);
+      for (int h = 0; h < kGroups; ++h) {
+        const int place = __shfl_sync(0xFFFFFFFFu, places, (fill.tile - places_tile) * kGroups + h);
+        const uint32_t bit = 1u << (kGroups * stage + h);
+        absent = place < 0 ? absent | bit : absent & ~bit;
+        const long long at = max(place, 0);
+        const uint32_t dst = ring_lane + stage * S::kBytes + h * S::kGroup;
 #pragma unroll
-      for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + S::kQ + 512 * i, vq_lane + at * S::kQ + 512 * i);
-      if (lane < 2 * SL) cp_async16(dst + 2 * S::kQ, sc_lane + at * S::kS);
+        for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + 512 * i, kq_lane + at * S::kQ + 512 * i);
+#pragma unroll
+        for (int i = 0; i < S::kQ / 512; ++i) cp_async16(dst + S::kQ + 512 * i, vq_lane + at * S::kQ + 512 * i);
+        if (lane < 2 * SL) cp_async16(dst + 2 * S::kQ, sc_lane + at * S::kS);
+      }
       --left;
       if (++fill.tile == fill.tiles) {
         kv_next<kTile>(a, fill, sched, seq0, nseq);
@@ -227,18 +234,20 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       fetch(stage == 0 ? kStages - 1 : stage - 1);
       cp_wait<kStages - 1>();
       __syncwarp();
-      const uint8_t* st = ring + stage * S::kBytes;
-      const bool live = !((absent >> stage) & 1u);
+      const uint8_t* st0 = ring + stage * S::kBytes;
+      const uint32_t gone = absent >> (kGroups * stage);
       stage = stage == kStages - 1 ? 0 : stage + 1;
       // MMA row r holds token r ^ ((r >> 1) & 1): the values' loads of four threads then fall on both
       // halves of the banks
       const int tok = g ^ ((g >> 1) & 1);
 
       // ---- scores
-      float s[NT][4];
+      float s[kGroups][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) s[nt][0] = s[nt][1] = s[nt][2] = s[nt][3] = 0.0f;
-      {
+      for (int h2 = 0; h2 < kGroups; ++h2) {
+        const uint8_t* st = st0 + h2 * S::kGroup;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) s[h2][nt][0] = s[h2][nt][1] = s[h2][nt][2] = s[h2][nt][3] = 0.0f;
         uint32_t kw[2][KW];
         uint32_t ks2[2][2];  // the scales of the thread's channels (first and second half of them), doubled
 #pragma unroll
@@ -273,23 +282,25 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
           for (int i = 0; i < 2; ++i) {
             const uint32_t af[4] = {h[0][2 * i], h[1][2 * i], h[0][2 * i + 1], h[1][2 * i + 1]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(s[nt], af, qf[nt][4 * w + 2 * i], qf[nt][4 * w + 2 * i + 1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(s[h2][nt], af, qf[nt][4 * w + 2 * i], qf[nt][4 * w + 2 * i + 1]);
           }
         }
       }
 
-      // ---- mask: only where some row's range ends inside the 16 tokens, or a page is missing
-      const int j0 = (use.first + tile) * kTile + my16;
-      if (!(live && j0 >= span.lo_all && j0 + 16 <= span.hi_all)) {
+      // ---- mask: only where some row's range ends inside the tokens, or a page is missing
+      const int j0 = (use.first + tile) * kTile + mine;
+      if ((gone & ((1u << kGroups) - 1u)) != 0u || j0 < span.lo_all || j0 + kWarpTokens > span.hi_all) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int h2 = 0; h2 < kGroups; ++h2)
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            const int r = 8 * nt + 2 * t + (c & 1), j = j0 + tok + (c >= 2 ? 8 : 0);
-            int lo, hi;
-            kv_row_range(a, span, r / p.group, lo, hi);
-            if (!(live && j >= lo && j < hi)) s[nt][c] = -INFINITY;
-          }
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int r = 8 * nt + 2 * t + (c & 1), j = j0 + 16 * h2 + tok + (c >= 2 ? 8 : 0);
+              int lo, hi;
+              kv_row_range(a, span, r / p.group, lo, hi);
+              if (((gone >> h2) & 1u) || j < lo || j >= hi) s[h2][nt][c] = -INFINITY;
+            }
       }
 
       // ---- running maximum (raised rarely), weights, sums
@@ -297,13 +308,13 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) up |= fmaxf(s[nt][c], s[nt][c + 2]) > raise[nt][c];
+        for (int c = 0; c < 2; ++c) up |= fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2])) > raise[nt][c];
       if (__any_sync(0xFFFFFFFFu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c) {
-            float m = fmaxf(s[nt][c], s[nt][c + 2]);
+            float m = fmaxf(fmaxf(s[0][nt][c], s[0][nt][c + 2]), fmaxf(s[1][nt][c], s[1][nt][c + 2]));
 #pragma unroll
             for (int x2 = 4; x2 < 32; x2 <<= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, x2));
             if (m > raise[nt][c]) {  // the same for the lanes that share the row
@@ -320,21 +331,25 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
             }
           }
       }
-      uint32_t pf[NT][2];
+      uint32_t pf[kGroups][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+      for (int h2 = 0; h2 < kGroups; ++h2)
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          w[c] = exp2_approx(__fmaf_rn(s[nt][c], cz[nt][c & 1], bias[nt][c & 1]));
-          sum[nt][c & 1] += w[c];
+        for (int nt = 0; nt < NT; ++nt) {
+          float w[4];
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            w[c] = exp2_approx(__fmaf_rn(s[h2][nt][c], cz[nt][c & 1], bias[nt][c & 1]));
+            sum[nt][c & 1] += w[c];
+          }
+          pf[h2][nt][0] = transpose8x8(f16x2_pack(w[0], w[1]));
+          pf[h2][nt][1] = transpose8x8(f16x2_pack(w[2], w[3]));
         }
-        pf[nt][0] = transpose8x8(f16x2_pack(w[0], w[1]));
-        pf[nt][1] = transpose8x8(f16x2_pack(w[2], w[3]));
-      }
 
       // ---- weighted sum of the values: tokens tA, tB (fragment columns 2 t, 2 t + 1) and 8 further on
-      {
+#pragma unroll
+      for (int h2 = 0; h2 < kGroups; ++h2) {
+        const uint8_t* st = st0 + h2 * S::kGroup;
         const int tA = 2 * t + (t & 1), tB = 2 * t + 1 - (t & 1);
         uint32_t vw[4][VW], vs2[2];
 #pragma unroll
@@ -369,7 +384,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
             const uint32_t af[4] = {f16x2_mul(h[0][0][i], vs2[0]), f16x2_mul(h[0][1][i], vs2[0]),
                                     f16x2_mul(h[1][0][i], vs2[1]), f16x2_mul(h[1][1][i], vs2[1])};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][4 * w + i], af, pf[nt][0], pf[nt][1]);
+            for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][4 * w + i], af, pf[h2][nt][0], pf[h2][nt][1]);
           }
         }
       }
