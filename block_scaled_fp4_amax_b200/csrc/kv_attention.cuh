@@ -211,9 +211,10 @@ __device__ __forceinline__ void kv_next(const KvAttentionLaunch& a, KvCursor& c,
 }
 
 // A unit that several CTAs hold parts of: the first part lies in slot `slot` of the CTA that began it,
-// the others in slot 0 of the CTAs after it.
-struct KvJoin {
-  int parts, seq, head, slot;
+// the others in slot 0 of the CTAs after it.  (16-byte aligned: two loads.)
+struct __align__(16) KvJoin {
+  int parts, rows, head, slot;
+  long long first_q, unused;
 };
 
 }  // namespace fp4k

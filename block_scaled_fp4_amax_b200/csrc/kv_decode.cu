@@ -115,7 +115,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   const int cta = blockIdx.x;
   const long long n = min((long long)gridDim.x, total);  // every CTA that works has a tile
   const long long x0 = cta < n ? cta * total / n : 0, x1 = cta < n ? (cta + 1) * total / n : 0;
-  KvJoin join = {0, 0, 0, 0};
+  KvJoin join = {0, 0, 0, 0, 0, 0};
 
   // The cursor that fills the ring runs ahead of the one that consumes it, across units.
   KvCursor fill, use;
@@ -441,7 +441,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       // this CTA holds the unit's first part: how many CTAs hold the rest, for the joining launch
       const long long end = x + (use.tiles - tile0);  // one past the unit's last tile
       const long long last = (end * n - 1) / total;   // the CTA that owns tile end - 1
-      join = {(int)(last - cta + 1), seq, head, (int)(slot & 1)};
+      join = {(int)(last - cta + 1), rows, head, (int)(slot & 1), span.first_q, 0};
     }
     __syncthreads();  // the merge area is free again
     x += tile1 - tile0;
@@ -452,65 +452,90 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
 }
 
 // Joins the parts of a unit: part 0 lies in the slot `join.slot` of the CTA that began the unit, the others
-// in slot 0 of the CTAs after it (up to a whole grid of them: one long sequence).  A block takes eight
-// rows, four warps a row; each warp adds every fourth part, D / 32 channels a lane.
-constexpr int kJoinRows = 8, kJoinWays = 4;
-template <int D>
-__global__ void __launch_bounds__(32 * kJoinRows * kJoinWays) kv_decode_join_kernel(DecodeParams p, int rows_cap) {
-  __shared__ float part[kJoinWays][kJoinRows][D], sums[kJoinWays][kJoinRows];
+// in slot 0 of the CTAs after it.  Most units have two or three parts, one long sequence's have a whole
+// grid of them, so four groups of 128 threads share them; a thread has four channels of every
+// fourth (D 128) or eighth (D 64) row, and eight parts' loads in flight: one trip to L2 for most units.
+constexpr int kJoinWays = 4, kJoinUnroll = 8;
+template <int D, int CAP>
+__global__ void __launch_bounds__(128 * kJoinWays) kv_decode_join_kernel(DecodeParams p) {
+  constexpr int C4 = D / 4, STEP = 128 / C4, ITEMS = CAP / STEP;  // rows a pass of 128 threads covers, passes
+  __shared__ float4 outs[kJoinWays - 1][CAP][C4];
+  __shared__ float2 mls[kJoinWays - 1][CAP];
   grid_dep_wait();
   const KvAttentionLaunch& a = p.a;
-  const int cta = blockIdx.x, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int r8 = warp % kJoinRows, way = warp / kJoinRows, r = blockIdx.y * kJoinRows + r8;
+  const int cta = blockIdx.x, way = threadIdx.x >> 7, c4 = threadIdx.x % C4, r0 = (threadIdx.x & 127) / C4;
   const KvJoin join = p.joins[cta];
   if (join.parts == 0) return;
-  const KvSpan span = kv_span(a, join.seq);
-  const bool have = r < span.queries * p.group;
-  constexpr int PER = D / 32;
-  float bias = -kNoMax;
-  if (have) {
-    const long long at0 = (2LL * cta + join.slot) * rows_cap + r, at1 = 2LL * (cta + 1) * rows_cap + r;
-    auto at = [&](int i) { return i == 0 ? at0 : at1 + 2LL * (i - 1) * rows_cap; };
-    for (int i = lane; i < join.parts; i += 32) bias = fminf(bias, p.part_ml[at(i)].x);
+  const long long at0 = (2LL * cta + join.slot) * CAP, at1 = 2LL * (cta + 1) * CAP;
+  float bias[ITEMS], l[ITEMS];
+  float4 v[ITEMS];
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) bias = fminf(bias, __shfl_xor_sync(0xFFFFFFFFu, bias, x));
-    float l = 0.0f, v[PER];
+  for (int k = 0; k < ITEMS; ++k) {
+    const int r = r0 + k * STEP;
+    bias[k] = -kNoMax;
+    l[k] = 0.0f;
+    v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (r >= join.rows) continue;
+    for (int i0 = way; i0 < join.parts; i0 += kJoinWays * kJoinUnroll) {
+      float2 ml[kJoinUnroll];
+      float4 o[kJoinUnroll];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) v[j] = 0.0f;
-#pragma unroll 4
-    for (int i = way; i < join.parts; i += kJoinWays) {
-      const float2 ml = p.part_ml[at(i)];
-      const float f = exp2_approx(bias - ml.x);
-      l += f * ml.y;
+      for (int u = 0; u < kJoinUnroll; ++u) {
+        const int i = i0 + u * kJoinWays;
+        const long long at = (i == 0 ? at0 : at1 + 2LL * (i - 1) * CAP) + r;
+        ml[u] = make_float2(-kNoMax, 0.0f);
+        o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (i < join.parts) {
+          ml[u] = p.part_ml[at];
+          o[u] = *reinterpret_cast<const float4*>(p.part + at * D + 4 * c4);
+        }
+      }
+      float b = bias[k];
 #pragma unroll
-      for (int j = 0; j < PER; j += 2) {
-        const float2 o = *reinterpret_cast<const float2*>(p.part + at(i) * D + lane * PER + j);
-        v[j] += f * o.x;
-        v[j + 1] += f * o.y;
+      for (int u = 0; u < kJoinUnroll; ++u) b = fminf(b, ml[u].x);
+      const float f = exp2_approx(b - bias[k]);
+      bias[k] = b;
+      l[k] *= f;
+      v[k].x *= f; v[k].y *= f; v[k].z *= f; v[k].w *= f;
+#pragma unroll
+      for (int u = 0; u < kJoinUnroll; ++u) {
+        const float w = exp2_approx(b - ml[u].x);
+        l[k] += w * ml[u].y;
+        v[k].x += w * o[u].x; v[k].y += w * o[u].y; v[k].z += w * o[u].z; v[k].w += w * o[u].w;
       }
     }
-#pragma unroll
-    for (int j = 0; j < PER; ++j) part[way][r8][lane * PER + j] = v[j];
-    if (lane == 0) sums[way][r8] = l;
+    if (way > 0) {
+      outs[way - 1][r][c4] = v[k];
+      if (c4 == 0) mls[way - 1][r] = make_float2(bias[k], l[k]);
+    }
   }
   __syncthreads();
-  if (!have || way != 0) return;
-  float l = 0.0f, v[PER];
+  if (way > 0) return;
+  const float gv = a.c.nv ? __ldg(a.c.v_global) : 1.0f;
 #pragma unroll
-  for (int j = 0; j < PER; ++j) v[j] = 0.0f;
+  for (int k = 0; k < ITEMS; ++k) {
+    const int r = r0 + k * STEP;
+    if (r >= join.rows) continue;
+    float b = bias[k];
 #pragma unroll
-  for (int w = 0; w < kJoinWays; ++w) {
-    l += sums[w][r8];
+    for (int w = 0; w < kJoinWays - 1; ++w) b = fminf(b, mls[w][r].x);
+    const float f = exp2_approx(b - bias[k]);
+    float sum = l[k] * f;
+    float4 o = make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) v[j] += part[w][r8][lane * PER + j];
+    for (int w = 0; w < kJoinWays - 1; ++w) {
+      const float2 ml = mls[w][r];
+      const float4 x = outs[w][r][c4];
+      const float g = exp2_approx(b - ml.x);
+      sum += g * ml.y;
+      o.x += g * x.x; o.y += g * x.y; o.z += g * x.z; o.w += g * x.w;
+    }
+    const int qi = r / p.group;
+    const long long row = (join.first_q + qi) * a.q_heads + join.head * p.group + (r - qi * p.group);
+    const float inv = kv_inverse(sum) * gv;
+    reinterpret_cast<uint2*>(a.out)[row * C4 + c4] = make_uint2(bf16x2_pack(o.x * inv, o.y * inv), bf16x2_pack(o.z * inv, o.w * inv));
+    if (a.lse && c4 == 0) a.lse[row] = kv_lse(b, sum);
   }
-  const int qi = r / p.group;
-  const long long row = (span.first_q + qi) * a.q_heads + join.head * p.group + (r - qi * p.group);
-  const float inv = kv_inverse(l) * (a.c.nv ? __ldg(a.c.v_global) : 1.0f);
-#pragma unroll
-  for (int j = 0; j < PER; j += 2)
-    reinterpret_cast<uint32_t*>(a.out)[(row * D + lane * PER + j) / 2] = bf16x2_pack(v[j] * inv, v[j + 1] * inv);
-  if (a.lse && lane == 0) a.lse[row] = kv_lse(bias, l);
 }
 
 template <int D, bool NV, int NT>
@@ -531,9 +556,7 @@ cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   kv_decode_kernel<D, NV, NT><<<dim3(n, chunks), 32 * kWarps, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  const int rows = min(p.a.max_q * p.group, 8 * NT);
-  return launch_pdl(kv_decode_join_kernel<D>, dim3(n * chunks, (rows + kJoinRows - 1) / kJoinRows),
-                    dim3(32 * kJoinRows * kJoinWays), 0, s, true, p, 8 * NT);
+  return launch_pdl(kv_decode_join_kernel<D, 8 * NT>, dim3(n * chunks), dim3(128 * kJoinWays), 0, s, true, p);
 }
 
 template <int D, bool NV>
