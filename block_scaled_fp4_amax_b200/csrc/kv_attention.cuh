@@ -210,11 +210,11 @@ __device__ __forceinline__ void kv_next(const KvAttentionLaunch& a, KvCursor& c,
   kv_tiles<TILE>(kv_span(a, seq0 + c.seq), c.first);
 }
 
-// A unit that several CTAs hold parts of: the first part lies in slot `slot` of the CTA that began it,
-// the others in slot 0 of the CTAs after it.  (16-byte aligned: two loads.)
+// A unit that several CTAs hold parts of (parts 0: none): the first part lies in slot `slot` of CTA `cta`,
+// which began it, the others in slot 0 of the CTAs after it.  (16-byte aligned: two loads.)
 struct __align__(16) KvJoin {
   int parts, rows, head, slot;
-  long long first_q, unused;
+  long long first_q, cta;
 };
 
 }  // namespace fp4k

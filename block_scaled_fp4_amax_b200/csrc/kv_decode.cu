@@ -54,7 +54,8 @@ struct DecodeParams {
   int chunk_seqs;  // sequences of a blockIdx.y
   float* part;     // partial outputs, [slot][row][D]
   float2* part_ml; // their maximum and sum, [slot][row]
-  KvJoin* joins;   // one per CTA
+  KvJoin* joins;   // one per unit, or, where there are more units than CTAs, one per CTA
+  bool by_unit;
   uint32_t* status;
 };
 
@@ -441,47 +442,54 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       // this CTA holds the unit's first part: how many CTAs hold the rest, for the joining launch
       const long long end = x + (use.tiles - tile0);  // one past the unit's last tile
       const long long last = (end * n - 1) / total;   // the CTA that owns tile end - 1
-      join = {(int)(last - cta + 1), rows, head, (int)(slot & 1), span.first_q, 0};
+      join = {(int)(last - cta + 1), rows, head, (int)(slot & 1), span.first_q, blockIdx.y * gridDim.x + cta};
+    }
+    if (p.by_unit && tile0 == 0 && threadIdx.x == 0) {
+      p.joins[(long long)seq * a.c.heads + head] = join;
+      join.parts = 0;
     }
     __syncthreads();  // the merge area is free again
     x += tile1 - tile0;
     use.tile = tile1;
     if (use.tile == use.tiles) kv_next<kTile>(a, use, sched, seq0, nseq);
   }
-  if (threadIdx.x == 0) p.joins[blockIdx.y * gridDim.x + cta] = join;
+  if (!p.by_unit && threadIdx.x == 0) p.joins[blockIdx.y * gridDim.x + cta] = join;
 }
 
 // Joins the parts of a unit: part 0 lies in the slot `join.slot` of the CTA that began the unit, the others
 // in slot 0 of the CTAs after it.  Most units have two or three parts, one long sequence's have a whole
-// grid of them, so four groups of 128 threads share them; a thread has four channels of every
-// fourth (D 128) or eighth (D 64) row, and eight parts' loads in flight: one trip to L2 for most units.
-constexpr int kJoinWays = 4, kJoinUnroll = 8;
-template <int D, int CAP>
-__global__ void __launch_bounds__(128 * kJoinWays) kv_decode_join_kernel(DecodeParams p) {
-  constexpr int C4 = D / 4, STEP = 128 / C4, ITEMS = CAP / STEP;  // rows a pass of 128 threads covers, passes
-  __shared__ float4 outs[kJoinWays - 1][CAP][C4];
-  __shared__ float2 mls[kJoinWays - 1][CAP];
+// grid of them, so WAYS groups of 128 threads share them; a thread has four channels of every
+// fourth (D 128) or eighth (D 64) row, and eight parts' loads in flight: one trip to L2 for most
+// units.  With SHARE a block takes one pass of 128 threads over the rows (blockIdx.y), else all.
+constexpr int kJoinUnroll = 4;
+template <int D, int CAP, int WAYS, bool SHARE>
+__global__ void __launch_bounds__(128 * WAYS) kv_decode_join_kernel(DecodeParams p) {
+  constexpr int C4 = D / 4, STEP = 128 / C4, ITEMS = SHARE ? 1 : CAP / STEP;  // rows a pass covers, passes
+  __shared__ float4 outs[WAYS - 1][ITEMS][STEP][C4];
+  __shared__ float2 mls[WAYS - 1][ITEMS][STEP];
   grid_dep_wait();
   const KvAttentionLaunch& a = p.a;
-  const int cta = blockIdx.x, way = threadIdx.x >> 7, c4 = threadIdx.x % C4, r0 = (threadIdx.x & 127) / C4;
-  const KvJoin join = p.joins[cta];
+  const int way = threadIdx.x >> 7, c4 = threadIdx.x % C4, r0 = (threadIdx.x & 127) / C4;
+  const KvJoin join = p.joins[blockIdx.x];
+  // (a sequence without queries has no CTA that writes its units' records)
+  if (p.by_unit && kv_span(a, blockIdx.x / a.c.heads).queries == 0) return;
   if (join.parts == 0) return;
-  const long long at0 = (2LL * cta + join.slot) * CAP, at1 = 2LL * (cta + 1) * CAP;
+  const long long at0 = (2LL * join.cta + join.slot) * CAP, at1 = 2LL * (join.cta + 1) * CAP;
   float bias[ITEMS], l[ITEMS];
   float4 v[ITEMS];
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
-    const int r = r0 + k * STEP;
+    const int r = r0 + (SHARE ? (int)blockIdx.y : k) * STEP;
     bias[k] = -kNoMax;
     l[k] = 0.0f;
     v[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (r >= join.rows) continue;
-    for (int i0 = way; i0 < join.parts; i0 += kJoinWays * kJoinUnroll) {
+    for (int i0 = way; i0 < join.parts; i0 += WAYS * kJoinUnroll) {
       float2 ml[kJoinUnroll];
       float4 o[kJoinUnroll];
 #pragma unroll
       for (int u = 0; u < kJoinUnroll; ++u) {
-        const int i = i0 + u * kJoinWays;
+        const int i = i0 + u * WAYS;
         const long long at = (i == 0 ? at0 : at1 + 2LL * (i - 1) * CAP) + r;
         ml[u] = make_float2(-kNoMax, 0.0f);
         o[u] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
@@ -505,8 +513,8 @@ __global__ void __launch_bounds__(128 * kJoinWays) kv_decode_join_kernel(DecodeP
       }
     }
     if (way > 0) {
-      outs[way - 1][r][c4] = v[k];
-      if (c4 == 0) mls[way - 1][r] = make_float2(bias[k], l[k]);
+      outs[way - 1][k][r0][c4] = v[k];
+      if (c4 == 0) mls[way - 1][k][r0] = make_float2(bias[k], l[k]);
     }
   }
   __syncthreads();
@@ -514,18 +522,18 @@ __global__ void __launch_bounds__(128 * kJoinWays) kv_decode_join_kernel(DecodeP
   const float gv = a.c.nv ? __ldg(a.c.v_global) : 1.0f;
 #pragma unroll
   for (int k = 0; k < ITEMS; ++k) {
-    const int r = r0 + k * STEP;
+    const int r = r0 + (SHARE ? (int)blockIdx.y : k) * STEP;
     if (r >= join.rows) continue;
     float b = bias[k];
 #pragma unroll
-    for (int w = 0; w < kJoinWays - 1; ++w) b = fminf(b, mls[w][r].x);
+    for (int w = 0; w < WAYS - 1; ++w) b = fminf(b, mls[w][k][r0].x);
     const float f = exp2_approx(b - bias[k]);
     float sum = l[k] * f;
     float4 o = make_float4(v[k].x * f, v[k].y * f, v[k].z * f, v[k].w * f);
 #pragma unroll
-    for (int w = 0; w < kJoinWays - 1; ++w) {
-      const float2 ml = mls[w][r];
-      const float4 x = outs[w][r][c4];
+    for (int w = 0; w < WAYS - 1; ++w) {
+      const float2 ml = mls[w][k][r0];
+      const float4 x = outs[w][k][r0][c4];
       const float g = exp2_approx(b - ml.x);
       sum += g * ml.y;
       o.x += g * x.x; o.y += g * x.y; o.z += g * x.z; o.w += g * x.w;
@@ -547,6 +555,7 @@ cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
   p.status = reinterpret_cast<uint32_t*>(ws);
   ws += kKvStatusBytes;
   p.joins = reinterpret_cast<KvJoin*>(ws);
+  p.by_unit = (long long)p.a.seqs * p.a.c.heads <= n * chunks;
   ws += (size_t)num_sms() * kMaxCtasPerSm * sizeof(KvJoin);
   p.part_ml = reinterpret_cast<float2*>(ws);
   ws += (size_t)num_sms() * kPartRowsPerSm * sizeof(float2);
@@ -556,7 +565,13 @@ cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   kv_decode_kernel<D, NV, NT><<<dim3(n, chunks), 32 * kWarps, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  return launch_pdl(kv_decode_join_kernel<D, 8 * NT>, dim3(n * chunks), dim3(128 * kJoinWays), 0, s, true, p);
+  // A block per unit where there are fewer units than CTAs (a grid of 592 blocks that find nothing to do
+  // costs 2 us); for few units more threads and blocks each.
+  constexpr int passes = 8 * NT * (D / 4) / 128;
+  const int records = p.by_unit ? p.a.seqs * p.a.c.heads : n * chunks;
+  if (p.by_unit && records <= num_sms() / 2)
+    return launch_pdl(kv_decode_join_kernel<D, 8 * NT, 8, true>, dim3(records, passes), dim3(1024), 0, s, true, p);
+  return launch_pdl(kv_decode_join_kernel<D, 8 * NT, 2, false>, dim3(records), dim3(256), 0, s, true, p);
 }
 
 template <int D, bool NV>
