@@ -39,14 +39,14 @@ constexpr int kStages = 2;
 
 // Rows a CTA handles (8 per n-tile) and CTAs per SM.
 template <int NT> struct DecodeCfg {
-  static constexpr int kCtas = NT == 1 ? 4 : 3;
+  static constexpr int kCtas = NT == 1 ? 4 : (NT == 2 ? 3 : 2);
 };
 
 constexpr int kMaxCtasPerSm = 4;
 // Rows of partial results an SM's CTAs may leave: two slots a CTA, 8 NT rows a slot.
-constexpr int kPartRowsPerSm = 3 * 2 * 16;
+constexpr int kPartRowsPerSm = 2 * 2 * 32;
 static_assert(DecodeCfg<1>::kCtas * 16 <= kPartRowsPerSm && DecodeCfg<2>::kCtas * 32 <= kPartRowsPerSm &&
-              DecodeCfg<1>::kCtas <= kMaxCtasPerSm && kKvDecodeRows == 16, "workspace");
+              DecodeCfg<4>::kCtas * 64 <= kPartRowsPerSm && DecodeCfg<1>::kCtas <= kMaxCtasPerSm && kKvDecodeRows == 32, "workspace");
 
 struct DecodeParams {
   KvAttentionLaunch a;
@@ -107,6 +107,9 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   uint8_t* ring = smem + warp * kStages * S::kBytes;
   float* merge = reinterpret_cast<float*>(smem + kWarps * kStages * S::kBytes);
   float2* merge_ml = reinterpret_cast<float2*>(merge + kWarps * 8 * NT * LD);
+  constexpr bool kQShared = NT > 2;
+  uint2* q_shared = reinterpret_cast<uint2*>(merge);
+  float* coef_shared = merge + NT * 32 * (D / 8);
 
   grid_dep_trigger();
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0u;  // no wait here can give up
@@ -180,10 +183,12 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
     const int tile1 = (int)min((long long)use.tiles, tile0 + (x1 - x));
 
     // queries: row 8 n + g, channels [t D/4, (t + 1) D/4), as fp16 fragments
-    uint32_t qf[NT][D / 8];
-    float coef[NT];  // of row 8 n + g: score in log2 units = sum * coef
+    // (in registers; past two n-tiles in shared memory, where the merge area lies, each warp filling one)
+    uint32_t qf[kQShared ? 1 : NT][D / 8];
+    float coef[kQShared ? 1 : NT];  // of row 8 n + g: score in log2 units = sum * coef
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int k = 0; k < (kQShared ? 1 : NT); ++k) {
+      const int nt = kQShared ? warp : k;
       const int r = 8 * nt + g;
       uint32_t raw[D / 8];
       uint32_t m = 0u;
@@ -205,17 +210,30 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       kv_query_scale(m, up, down);
       float c = a.scale * 1.44269504f * (NV ? __ldg(a.c.k_global) : 1.0f) * down;
       kv_positive(c, up);
-      coef[nt] = c;
+      coef[k] = c;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i)
-        qf[nt][i] = f16x2_pack(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xFFFF0000u) * up);
+        qf[k][i] = f16x2_pack(__uint_as_float(raw[i] << 16) * up, __uint_as_float(raw[i] & 0xFFFF0000u) * up);
     }
     // the coefficients of this lane's score columns (rows 8 n + 2 t and 8 n + 2 t + 1)
     float cz[NT][2];
+    if constexpr (kQShared) {
+      if (warp < NT) {
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      cz[nt][0] = __shfl_sync(0xFFFFFFFFu, coef[nt], 8 * t);
-      cz[nt][1] = __shfl_sync(0xFFFFFFFFu, coef[nt], 8 * t + 4);
+        for (int i = 0; i < D / 16; ++i) q_shared[(warp * (D / 16) + i) * 32 + lane] = make_uint2(qf[0][2 * i], qf[0][2 * i + 1]);
+        if (t == 0) coef_shared[8 * warp + g] = coef[0];
+      }
+      __syncthreads();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) cz[nt][c] = coef_shared[8 * nt + 2 * t + c];
+    } else {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        cz[nt][0] = __shfl_sync(0xFFFFFFFFu, coef[nt], 8 * t);
+        cz[nt][1] = __shfl_sync(0xFFFFFFFFu, coef[nt], 8 * t + 4);
+      }
     }
 
     // weights are exp2(sum * cz + bias); `raise` is the sum past which the bias changes
@@ -283,7 +301,14 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
           for (int i = 0; i < 2; ++i) {
             const uint32_t af[4] = {h[0][2 * i], h[1][2 * i], h[0][2 * i + 1], h[1][2 * i + 1]};
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) mma_f16(s[h2][nt], af, qf[nt][4 * w + 2 * i], qf[nt][4 * w + 2 * i + 1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              if constexpr (kQShared) {
+                const uint2 b = q_shared[(nt * (D / 16) + 2 * w + i) * 32 + lane];
+                mma_f16(s[h2][nt], af, b.x, b.y);
+              } else {
+                mma_f16(s[h2][nt], af, qf[nt][4 * w + 2 * i], qf[nt][4 * w + 2 * i + 1]);
+              }
+            }
           }
         }
       }
@@ -393,6 +418,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
     }
 
     // ---------------------------------------------------------------- join the four warps
+    if constexpr (kQShared) __syncthreads();  // every warp is done with the queries
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -578,7 +604,9 @@ template <int D, bool NV>
 cudaError_t decode_rows(DecodeParams& p, cudaStream_t s) {
   const int rows = p.a.max_q * p.group;
   if (rows <= 8) return decode_t<D, NV, 1>(p, s);
-  return decode_t<D, NV, 2>(p, s);
+  if (rows <= 16) return decode_t<D, NV, 2>(p, s);
+  if (rows <= 24) return decode_t<D, NV, 3>(p, s);
+  return decode_t<D, NV, 4>(p, s);
 }
 
 }  // namespace

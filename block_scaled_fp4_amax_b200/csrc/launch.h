@@ -154,7 +154,7 @@ cudaError_t launch_kv_attention(const KvAttentionLaunch& L, cudaStream_t s);
 size_t kv_attention_workspace();
 // The kernels behind it.  kv_decode: at most kKvDecodeRows rows (queries x query heads) a key/value head.
 // Both keep a 32-bit status word at the start of the workspace (0: every wait ended).
-constexpr int kKvDecodeRows = 16;
+constexpr int kKvDecodeRows = 32;
 constexpr size_t kKvStatusBytes = 256;
 cudaError_t launch_kv_decode(const KvAttentionLaunch& L, cudaStream_t s);
 cudaError_t launch_kv_prompt(const KvAttentionLaunch& L, cudaStream_t s);
