@@ -10,7 +10,9 @@
 //                   a thread), two stages each, shared by both row tiles and all the group's heads;
 //   warp 12         issues the MMAs: S = Q K^T (both operands in shared memory, 128-byte swizzle, K-major)
 //                   and O += P V (P in tensor memory, V as it lies: tokens x channels, N-major).
-// While one row tile is in its softmax the tensor cores work on the other.  Tensor memory holds two
+// While one row tile is in its softmax the tensor cores work on the other.  With at most 128 rows the second
+// tile takes the same rows and every other step of the keys, and the two are added at the end (80 rows
+// over 6001 tokens: SINGLE us with one tile, TWIN us so).  Tensor memory holds two
 // score tiles (128 columns each) and two output tiles (head_dim columns each).
 //
 // Numerics are those of kv_decode.cu: v * d and the power-of-two scaled queries are exact in fp16, the
@@ -80,6 +82,19 @@ __host__ __device__ constexpr uint32_t idesc_prompt(int n, bool b_mn) {
   return (1u << 4) | ((b_mn ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
 }
 
+// 32 columns of this warp's rows of an output tile; zeros where no step wrote it.
+__device__ __forceinline__ void load_rows(uint32_t taddr, bool written, uint32_t (&o)[32]) {
+  if (written) {
+    TC_LD32(taddr, o);
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) o[j] = 0u;
+  }
+#pragma unroll
+  for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(o[j]));  // not used before the wait
+}
+
 // Where the CTA works: unit and its keys.
 struct Unit {
   int seq, head, row0, rows;  // rows here (at most 256) of the sequence's queries x group
@@ -135,7 +150,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
   uint8_t* pages_of = base + L::kBars + 128;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int mtiles = u.rows > 128 ? 2 : 1;
+  const bool twin = u.rows <= 128;  // both tiles hold the same rows; tile m takes the steps k = m, m + 2, ...
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + 8 * i, 128);
@@ -145,7 +160,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, 128);
     }
-    mbar_init(q_ready, 128 * mtiles);
+    mbar_init(q_ready, twin ? 128 : 256);
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -165,8 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
     // ------------------------------------------------------------------ softmax: a row a thread
     regs_inc<192>();
     const int m = warp >> 2;
-    if (m < mtiles) {
-      const int r = threadIdx.x & 127, row = 128 * m + r;
+    {
+      const int r = threadIdx.x & 127, row = (twin ? 0 : 128 * m) + r;
+      const bool warp_live = row - lane < u.rows;  // some row of this warp exists
       const bool have = row < u.rows;
       const int at = u.row0 + (have ? row : 0);
       const int qi = at / p.group, hq = u.head * p.group + (at - qi * p.group);
@@ -190,6 +206,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         const uint32_t q_tile = smem + L::kQ + m * L::kTile;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
+          if (twin && m == 1) break;  // the first tile's warps store them
           uint32_t h[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -198,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      mbar_arrive(q_ready);
+      if (!twin || m == 0) mbar_arrive(q_ready);
 
       int lo, hi;
       kv_row_range(a, span, qi, lo, hi);
@@ -207,9 +224,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       float mx = kNoMax;
       f32x2 sums[4] = {0ull, 0ull, 0ull, 0ull};
       bool ok = true;
-      for (int k = 0; k < n; ++k) {
-        if (!warp_wait(s_full + 8 * m, k & 1, abort_flag, p.status, 0, p.wait_ns)) { ok = false; break; }
+      int turn = 0;  // steps of this tile so far
+      for (int k = twin ? m : 0; k < n; k += twin ? 2 : 1, ++turn) {
+        if (!warp_wait_short(s_full + 8 * m, turn & 1, abort_flag, p.status, 0, p.wait_ns)) { ok = false; break; }
         tc_fence_after();
+        if (!warp_live) {  // rows that nobody reads
+          mbar_arrive(p_ready + 8 * m);
+          continue;
+        }
         uint32_t s[128];
         TC_LD32(t_s, (&s[0]));
         TC_LD32(t_s + 32, (&s[32]));
@@ -246,7 +268,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
           mx = to;
 #pragma unroll
           for (int j = 0; j < 4; ++j) sums[j] = f2_mul(sums[j], f2_pack(f, f));
-          if (k > 0) {
+          if (turn > 0) {
 #pragma unroll 1
             for (int c = 0; c < D; c += 32) {
               uint32_t o[32];
@@ -280,27 +302,58 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         tc_fence_before();
         mbar_arrive(p_ready + 8 * m);
       }
-      if (ok && n > 0) ok = warp_wait(o_full, 0, abort_flag, p.status, 1, p.wait_ns);
+      if (ok && n > 0) ok = warp_wait_short(o_full, 0, abort_flag, p.status, 1, p.wait_ns);
       tc_fence_after();
-      if (ok) {
-        float s0, s1;
-        f2_unpack(f2_add(f2_add(sums[0], sums[1]), f2_add(sums[2], sums[3])), s0, s1);
-        const float sum = s0 + s1;
+      float s0, s1;
+      f2_unpack(f2_add(f2_add(sums[0], sums[1]), f2_add(sums[2], sums[3])), s0, s1);
+      float sum = s0 + s1;
+      // one tile's rows: the second tile's warps leave their part in shared memory, where the keys were (no
+      // MMA is left that reads them), and the first tile's warps add it
+      const uint32_t other_o = smem + L::kK + r * 16, other_ms = smem + L::kV + r * 8;
+      float f_mine = 1.0f, f_other = 0.0f;
+      if (twin) {
+        if (m == 1) {
+          if (ok && warp_live) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+              uint32_t o[32];
+              load_rows(t_o + c, turn > 0, o);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) st_shared16(other_o + (c / 4 + j) * (128 * 16), o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+            }
+            asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(other_ms), "f"(mx), "f"(sum) : "memory");
+          }
+        }
+        asm volatile("bar.sync 1, 256;" ::: "memory");  // every warp of both tiles, whether it gave up or not
+        ok = __all_sync(0xFFFFFFFFu, ok && !*abort_flag);
+        if (m == 0 && ok && warp_live) {
+          float mx1, sum1;
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(mx1), "=f"(sum1) : "r"(other_ms) : "memory");
+          const float top = fmaxf(mx, mx1);
+          f_mine = exp2_approx(mx - top);
+          f_other = exp2_approx(mx1 - top);
+          mx = top;
+          sum = sum * f_mine + sum1 * f_other;
+        }
+      }
+      if (ok && warp_live && !(twin && m == 1)) {
         const float inv = kv_inverse(sum) * (NV ? __ldg(a.c.v_global) : 1.0f);
         const long long out_row = (span.first_q + qi) * a.q_heads + hq;
         const long long part_row = u.slot * kRows + row;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
-          if (n > 0) {
-            TC_LD32(t_o + c, o);
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-          } else {
+          load_rows(t_o + c, turn > 0, o);
+          if (twin) {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) o[j] = 0u;
+            for (int j = 0; j < 8; ++j) {
+              float x[4];
+              asm volatile("ld.shared.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3])
+                           : "r"(other_o + (c / 4 + j) * (128 * 16)) : "memory");
+#pragma unroll
+              for (int i = 0; i < 4; ++i) o[4 * j + i] = __float_as_uint(__uint_as_float(o[4 * j + i]) * f_mine + x[i] * f_other);
+            }
           }
-#pragma unroll
-          for (int j = 0; j < 32; ++j) asm volatile("" : "+r"(o[j]));
           if (have && p.splits == 1) {
             uint4* dst = reinterpret_cast<uint4*>(reinterpret_cast<__nv_bfloat16*>(a.out) + out_row * D + c);
 #pragma unroll
@@ -383,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
     for (int k = 0; k < n; ++k) {
       const int st = k & 1;
       const uint32_t free_parity = ((k >> 1) & 1) ^ 1;
-      if (!warp_wait(k_empty + 8 * st, free_parity, abort_flag, p.status, 2, p.wait_ns)) break;
+      if (!warp_wait_short(k_empty + 8 * st, free_parity, abort_flag, p.status, 2, p.wait_ns)) break;
       const uint32_t groups = __ballot_sync(0xFFFFFFFFu, live);
       if (lane == 0) pages_of[4 * (k & 3) + (warp & 3)] = (uint8_t)((groups & 1u) | ((groups >> 15) & 2u));
       expand(smem + L::kK + st * L::kTile, kw, ksc, false);
@@ -392,7 +445,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       locate(k + 1, next_id);
       next_id = page_id(k + 2);
       if (k + 1 < n) load(kw, ksc, a.c.kq, a.c.ks);
-      if (!warp_wait(v_empty + 8 * st, free_parity, abort_flag, p.status, 3, p.wait_ns)) break;
+      if (!warp_wait_short(v_empty + 8 * st, free_parity, abort_flag, p.status, 3, p.wait_ns)) break;
       expand(smem + L::kV + st * L::kTile, vw, vsc, true);
       mbar_arrive(v_full + 8 * st);
       if (k + 1 < n) load(vw, vsc, a.c.vq, a.c.vs);
@@ -404,9 +457,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       const bool lead = elect_one();
       const uint32_t i_s = idesc_prompt(kKeys, false), i_o = idesc_prompt(D, true);
       bool ok = n > 0;
+      // scores of step k into tile m
       auto scores = [&](int m, int k) {
         if (lead) {
-          const uint32_t q = smem + L::kQ + m * L::kTile, kt = smem + L::kK + (k & 1) * L::kTile;
+          const uint32_t q = smem + L::kQ + (twin ? 0 : m) * L::kTile, kt = smem + L::kK + (k & 1) * L::kTile;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t off = (i >> 2) * (128 * 128) + (i & 3) * 32;
@@ -415,35 +469,62 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
           tc_commit(s_full + 8 * m);
         }
       };
-      if (ok) ok = mbar_wait(q_ready, 0, abort_flag, p.status, 4, p.wait_ns) &&
-                   mbar_wait(k_full, 0, abort_flag, p.status, 5, p.wait_ns);
-      if (ok) {
-        tc_fence_after();
-        for (int m = 0; m < mtiles; ++m) scores(m, 0);
-        if (lead) tc_commit(k_empty);
-      }
-      for (int k = 0; k < n && ok; ++k) {
-        const int st = k & 1;
-        if (!mbar_wait(v_full + 8 * st, (k >> 1) & 1, abort_flag, p.status, 6, p.wait_ns)) { ok = false; break; }
-        if (k + 1 < n && !mbar_wait(k_full + 8 * (st ^ 1), ((k + 1) >> 1) & 1, abort_flag, p.status, 5, p.wait_ns)) { ok = false; break; }
-        for (int m = 0; m < mtiles; ++m) {
-          if (!mbar_wait(p_ready + 8 * m, k & 1, abort_flag, p.status, 7, p.wait_ns)) { ok = false; break; }
-          tc_fence_after();
-          if (lead) {
-            const uint32_t vt = smem + L::kV + st * L::kTile;
-#pragma unroll
-            for (int i = 0; i < kKeys / 16; ++i)
-              tc_mma_f16_ts(tmem + 256 + D * m, tmem + 128 * m + 8 * i, desc_sw128_mn(vt + i * 2048, 128 * 128), i_o, k > 0 || i > 0);
-          }
-          if (k + 1 < n) scores(m, k + 1);
-        }
-        if (!ok) break;
+      // product of tile m's weights with the values of step k; `first`: of the tile
+      auto product = [&](int m, int k, bool first) {
         if (lead) {
-          tc_commit(v_empty + 8 * st);
-          if (k + 1 < n) tc_commit(k_empty + 8 * (st ^ 1));
-          else tc_commit(o_full);
+          const uint32_t vt = smem + L::kV + (k & 1) * L::kTile;
+#pragma unroll
+          for (int i = 0; i < kKeys / 16; ++i)
+            tc_mma_f16_ts(tmem + 256 + D * m, tmem + 128 * m + 8 * i, desc_sw128_mn(vt + i * 2048, 128 * 128), i_o, !first || i > 0);
+        }
+      };
+      auto keys = [&](int k) { return mbar_wait_short(k_full + 8 * (k & 1), (k >> 1) & 1, abort_flag, p.status, 5, p.wait_ns); };
+      auto values = [&](int k) { return mbar_wait_short(v_full + 8 * (k & 1), (k >> 1) & 1, abort_flag, p.status, 6, p.wait_ns); };
+      auto weights = [&](int m, int turn) { return mbar_wait_short(p_ready + 8 * m, turn & 1, abort_flag, p.status, 7, p.wait_ns); };
+      auto release = [&](uint32_t bar) { if (lead) tc_commit(bar); };
+      if (ok) ok = mbar_wait_short(q_ready, 0, abort_flag, p.status, 4, p.wait_ns);
+      if (twin) {
+        for (int k = 0; k < min(n, 2) && ok; ++k) {
+          if (!keys(k)) { ok = false; break; }
+          tc_fence_after();
+          scores(k, k);
+          release(k_empty + 8 * k);
+        }
+        for (int k = 0; k < n && ok; ++k) {
+          const int m = k & 1;
+          if (!values(k) || !weights(m, k >> 1)) { ok = false; break; }
+          tc_fence_after();
+          product(m, k, k < 2);
+          release(v_empty + 8 * m);
+          if (k + 2 < n) {
+            if (!keys(k + 2)) { ok = false; break; }
+            tc_fence_after();
+            scores(m, k + 2);
+            release(k_empty + 8 * m);
+          }
+        }
+      } else {
+        if (ok) ok = keys(0);
+        if (ok) {
+          tc_fence_after();
+          scores(0, 0);
+          scores(1, 0);
+          release(k_empty);
+        }
+        for (int k = 0; k < n && ok; ++k) {
+          if (!values(k) || (k + 1 < n && !keys(k + 1))) { ok = false; break; }
+          for (int m = 0; m < 2; ++m) {
+            if (!weights(m, k)) { ok = false; break; }
+            tc_fence_after();
+            product(m, k, k == 0);
+            if (k + 1 < n) scores(m, k + 1);
+          }
+          if (!ok) break;
+          release(v_empty + 8 * (k & 1));
+          if (k + 1 < n) release(k_empty + 8 * ((k + 1) & 1));
         }
       }
+      if (ok) release(o_full);
       if (lead) {
         // on every path: no MMA is in flight when tensor memory is freed
         tc_commit(drain);

@@ -391,7 +391,12 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  *   Limits: total_q <= 2^24, seqs <= 32768, max_pages * page_size <= 2^30, q_heads <= 4096.
  *   lse   : device float [total_q, q_heads] or NULL: natural log of the sum of exp(scale q k).
  *   workspace : device, 16-byte aligned, >= fp4_workspace_size(FP4_OP_KV_ATTENTION, total_q, q_heads)
- *           bytes; clobbered, needs no initialisation.  Calls that overlap need one each. */
+ *           bytes; clobbered, needs no initialisation.  Calls that overlap need one each.  Its first 4
+ *           bytes are a status word, 0 when every pipeline wait of the call ended; otherwise bit i
+ *           names the wait that gave up (many rows only: 0 scores, 1 the output, 2 and 3 a free key
+ *           and value stage, 4 the queries, 5 and 6 a full key and value stage, 7 weights) and the
+ *           output is incomplete.  The limit is that of fp4_set_gemm_wait_limit.
+ * No gradients: a cache in 4 bits serves inference. */
 FP4_API fp4_status fp4_kv_attention(const void* q, fp4_dtype dtype, long total_q, long q_stride,
                                     long q_head_stride, int q_heads, const unsigned char* kq,
                                     const unsigned char* ks, const unsigned char* vq, const unsigned char* vs,
@@ -414,7 +419,8 @@ FP4_API size_t fp4_workspace_size(fp4_op op, long rows, long cols);
 FP4_API size_t fp4_gemm_status_word(void);
 
 /* Limit, in nanoseconds, of each pipeline wait inside the GEMM kernels launched after this call
- * (fp4_block_gemm, fp4_block_gemm_e4m3); returns the previous limit.  The default is 2000000000
+ * (fp4_block_gemm, fp4_block_gemm_e4m3) and inside fp4_kv_attention's kernel for many rows; returns
+ * the previous limit.  The default is 2000000000
  * (2 s), far above any wait of a working pipeline.  A small limit makes the kernel give up early,
  * which is how the fault path is exercised without faulting: 0 gives up at the first wait that has
  * not completed already.  Process-wide; launches already enqueued keep their limit. */

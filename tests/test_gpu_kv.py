@@ -404,3 +404,176 @@ def test_offsets_beyond_32_bits(cuda):
     assert torch.equal(a, b)
     want, _ = quantise(x[0].float().cpu().numpy(), fp4.NVFP4, 0.0021)
     assert np.array_equal(cache[0][pages - 1, :, :20].transpose(0, 1).cpu().numpy(), want)
+
+
+# ---------------------------------------------------------------------------------------------
+# calls at the edges of the kernels' rules
+
+@pytest.mark.parametrize("queries,group,heads,length", [
+    (16, 1, 2, 300), (17, 1, 2, 300), (6, 4, 1, 1000), (8, 4, 1, 129), (33, 1, 1, 5000), (16, 8, 1, 6000),   # rows 16 .. 128
+    (43, 3, 2, 400), (64, 4, 1, 200), (257, 1, 1, 260), (40, 13, 1, 3000)])                                  # and past
+def test_row_counts(cuda, queries, group, heads, length):
+    """Rows a head on both sides of every kernel's limit, one to many splits of the keys."""
+    for fmt, dim in ((fp4.NVFP4, 128), (fp4.MXFP4, 64)):
+        c = Cache([length], heads, dim, 16, fmt, seed=queries)
+        run_and_check(c, [queries], group)
+        run_and_check(c, [queries], group, window=length // 3 + 1)
+
+
+@pytest.mark.parametrize("queries", [1, 4, 40])
+def test_sequences_without_queries_or_keys(cuda, queries):
+    c = Cache([300, 0, 77, 500, 12, 0], 2, 64, 16, fp4.NVFP4, seed=2)
+    run_and_check(c, [queries, 1, 0, queries, 0, 0], 4)
+    run_and_check(c, [0, 0, 0, queries, 0, 0], 4)
+
+
+@pytest.mark.parametrize("seqs,heads,long", [(90, 8, 3000), (300, 2, 700), (600, 1, 90)])
+def test_many_sequences(cuda, seqs, heads, long):
+    """More units than resident blocks, and more sequences than one schedule holds."""
+    lens = [long] + [(37 * i) % 60 for i in range(1, seqs)]
+    c = Cache(lens, heads, 64, 16, fp4.NVFP4, seed=3)
+    run_and_check(c, [1] * seqs, 2)
+
+
+def test_many_sequences_of_many_rows(cuda):
+    lens = [150 + (37 * i) % 60 for i in range(70)]
+    c = Cache(lens, 1, 64, 16, fp4.MXFP4, seed=3)
+    run_and_check(c, [20 + i % 30 for i in range(70)], 2)
+
+
+@pytest.mark.parametrize("queries", [1, 12, 48])
+def test_layouts(cuda, queries):
+    """Head-major queries, a block table that is a slice of a wider one, one head of many."""
+    c = Cache([130, 61], 2, 128, 16, fp4.NVFP4, seed=5)
+    q = torch.randn(2 * queries, 8, 128, device=cuda).to(torch.bfloat16)
+    want, lse = fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, max_q=queries, want_lse=True, **c.scales)
+    head_major = q.transpose(0, 1).contiguous().transpose(0, 1)
+    wide = torch.full((2, c.table.shape[1] + 7), -1, dtype=torch.int32, device=cuda)
+    wide[:, :c.table.shape[1]] = c.table
+    out, l2 = fp4.fp4_kv_attention(head_major, c.arrays, wide[:, :c.table.shape[1]], c.lens_t, max_q=queries, want_lse=True,
+                                   workspace=torch.full((fp4.workspace_size(fp4.OP_KV_ATTENTION),), 0xFF, dtype=torch.uint8, device=cuda),
+                                   **c.scales)
+    assert torch.equal(out, want) and torch.equal(l2, lse)
+
+
+def test_mx_scale_bytes_outside_the_cache_range(cuda):
+    """Bytes 0..103 count as 104 in attention, 141..255 as 140."""
+    c = Cache([40], 1, 64, 16, fp4.MXFP4)
+    q = torch.randn(1, 4, 64, device=cuda).to(torch.bfloat16)
+    for which in (1, 3):
+        got = []
+        for byte in (0, 104, 140, 200, 255):
+            arrays = [a.clone() for a in c.arrays]
+            arrays[which][int(c.table_np[0, 1]), 0, 3, 0] = byte
+            got.append(torch.cat([fp4.fp4_kv_attention(q.expand(m, 4, 64).contiguous(), arrays, c.table, c.lens_t, fp4.MXFP4, max_q=m)[0] for m in (1, 40)]))
+        assert torch.equal(got[0], got[1]) and torch.equal(got[2], got[3]) and torch.equal(got[2], got[4])
+
+
+def test_two_calls_at_once(cuda):
+    """Two streams, each with calls of its own (workspaces of the binding's making)."""
+    cases = [_decode_case(cuda, s, [2500, 64, 700]) for s in (3, 4)]
+    want = [fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, **c.scales)[0] for c, q in cases]
+    prompts = [torch.randn(3 * 50, 8, 128, device=cuda).to(torch.bfloat16) for _ in cases]
+    pwant = [fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, max_q=50, **c.scales)[0] for (c, _), q in zip(cases, prompts)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got, pgot = [], []
+    for _ in range(4):
+        for s, (c, q), pq in zip(streams, cases, prompts):
+            got.append(fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, stream=s, **c.scales)[0])
+            pgot.append(fp4.fp4_kv_attention(pq, c.arrays, c.table, c.lens_t, max_q=50, stream=s, **c.scales)[0])
+    torch.cuda.synchronize()
+    for i, (a, b) in enumerate(zip(got, pgot)):
+        assert torch.equal(a, want[i % 2]) and torch.equal(b, pwant[i % 2])
+
+
+def test_prompt_graph_and_append_in_it(cuda):
+    """A captured step of append and attention, single tokens and a chunk, replayed on new inputs."""
+    sc = scales_for(fp4.NVFP4, cuda)
+    cache = sentinel_cache(20, 2, 16, 128, fp4.NVFP4, cuda)
+    table = torch.arange(20, dtype=torch.int32, device=cuda).view(2, 10)
+    for new in (1, 24):
+        qkv = torch.zeros(2 * new, 12, 128, dtype=torch.bfloat16, device=cuda)
+        slots = torch.zeros(2 * new, dtype=torch.int64, device=cuda)
+        lens = torch.zeros(2, dtype=torch.int32, device=cuda)
+
+        def step():
+            fp4.fp4_kv_append(qkv[:, 8:10], qkv[:, 10:], cache, slots, **sc)
+            return fp4.fp4_kv_attention(qkv[:, :8], cache, table, lens, max_q=new, **sc)[0]
+
+        def fill(past):
+            qkv.copy_(torch.randn(2 * new, 12, 128, device=cuda))
+            pos = torch.arange(past, past + new, device=cuda)
+            slots.copy_(torch.cat([table[b].long()[pos // 16] * 16 + pos % 16 for b in range(2)]))
+            lens.fill_(past + new)
+
+        fill(0)
+        step()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = step()
+        for past in (0, new, 2 * new):
+            fill(past)
+            g.replay()
+            torch.cuda.synchronize()
+            got = out.clone()
+            assert torch.equal(step(), got)
+
+
+def test_wait_limit_reports_and_recovers(cuda):
+    """A limit of 0 ns makes the many-row kernel's first unfinished wait give up: the status word says so,
+    the call returns, and the next call is right."""
+    c = Cache([700], 1, 128, 16, fp4.NVFP4)
+    q = torch.randn(300, 4, 128, device=cuda).to(torch.bfloat16)
+    ws = torch.zeros(fp4.workspace_size(fp4.OP_KV_ATTENTION), dtype=torch.uint8, device=cuda)
+    old = fp4.set_gemm_wait_limit(0)
+    try:
+        fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, max_q=300, workspace=ws, **c.scales)
+        torch.cuda.synchronize()
+    finally:
+        fp4.set_gemm_wait_limit(old)
+    assert int(ws[:4].view(torch.int32)) != 0
+    want, _ = fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, max_q=300, workspace=ws, **c.scales)
+    assert int(ws[:4].view(torch.int32)) == 0
+    run_and_check(c, [300], 4)
+    assert bool(torch.isfinite(want.float()).all())
+
+
+def test_binding_refusals(cuda):
+    c = Cache([40], 2, 64, 16, fp4.NVFP4)
+    q = torch.randn(1, 4, 64, device=cuda).to(torch.bfloat16)
+    k = torch.randn(3, 2, 64, device=cuda).to(torch.bfloat16)
+    slots = torch.arange(3, device=cuda)
+
+    def attend(**kw):
+        a = dict(q=q, cache=c.arrays, table=c.table, lens=c.lens_t, **c.scales)
+        a.update(kw)
+        return fp4.fp4_kv_attention(a.pop("q"), a.pop("cache"), a.pop("table"), a.pop("lens"), **a)
+
+    for err, kw in [(TypeError, dict(q=q.half())), (fp4.Fp4Error, dict(q=q.float())), (ValueError, dict(q=q[..., :32])),
+                    (ValueError, dict(q=q.cpu())), (ValueError, dict(q=q.expand(2, 1, 4, 64))), (fp4.Fp4Error, dict(q=q[:, :3])),
+                    (ValueError, dict(table=c.table.long())), (ValueError, dict(table=c.table[:, ::2])), (ValueError, dict(lens=c.lens_t.cpu())),
+                    (ValueError, dict(lens=c.lens_t.long())), (ValueError, dict(cu_q=c.lens_t)), (fp4.Fp4Error, dict(max_q=2)),
+                    (fp4.Fp4Error, dict(scale=float("nan"))), (ValueError, dict(out=torch.empty_like(q).float())),
+                    (fp4.Fp4Error, dict(workspace=torch.empty(16, dtype=torch.uint8, device=cuda))), (fp4.Fp4Error, dict(k_global=None)),
+                    (ValueError, dict(k_global=torch.ones(2, device=cuda))), (ValueError, dict(cache=c.arrays[:3] + (c.arrays[3][:1],))),
+                    (ValueError, dict(fmt=fp4.MXFP4)), (fp4.Fp4Error, dict(fmt=fp4.IF4)), (TypeError, dict(window=1.5)),
+                    (ValueError, dict(max_q=2 ** 40)), (TypeError, dict(lens=[40]))]:
+        with pytest.raises(err):
+            attend(**kw)
+    for err, args in [(ValueError, (k, k.float(), c.arrays, slots)), (ValueError, (k, k[:2], c.arrays, slots)), (TypeError, (k.half(), k.half(), c.arrays, slots)),
+                      (ValueError, (k, k, c.arrays, slots.int())), (ValueError, (k, k, c.arrays, slots[:2])), (ValueError, (k[:, :1], k[:, :1], c.arrays, slots)),
+                      (ValueError, (k.transpose(1, 2).contiguous().transpose(1, 2), k, c.arrays, slots))]:
+        with pytest.raises(err):
+            fp4.fp4_kv_append(*args, **c.scales)
+    with pytest.raises(fp4.Fp4Error):   # rows that start off a 32-byte boundary
+        odd = torch.randn(3, 2 * 64 + 4, device=cuda).to(torch.bfloat16)[:, 4:].unflatten(1, (2, 64))
+        fp4.fp4_kv_append(odd, k, c.arrays, slots, **c.scales)
+    cu = torch.tensor([0, 40], dtype=torch.int32, device=cuda)
+    for err, kw in [(ValueError, dict(cu=cu.long())), (ValueError, dict(starts=cu)), (TypeError, dict(out_dtype=torch.float16)),
+                    (ValueError, dict(out=(torch.empty(40, 2, 64, device=cuda),) * 1 + (torch.empty(39, 2, 64, device=cuda),)))]:
+        a = dict(cu=cu)
+        a.update(kw)
+        with pytest.raises(err):
+            fp4.fp4_kv_read(c.arrays, c.table, a.pop("cu"), 40, **a, **c.scales)
