@@ -12,7 +12,7 @@
 //                   and O += P V (P in tensor memory, V as it lies: tokens x channels, N-major).
 // While one row tile is in its softmax the tensor cores work on the other.  With at most 128 rows the second
 // tile takes the same rows and every other step of the keys, and the two are added at the end (80 rows
-// over 6001 tokens: SINGLE us with one tile, TWIN us so).  Tensor memory holds two
+// over 6001 tokens: 92 us with one tile, 72 us so).  Tensor memory holds two
 // score tiles (128 columns each) and two output tiles (head_dim columns each).
 //
 // Numerics are those of kv_decode.cu: v * d and the power-of-two scaled queries are exact in fp16, the
@@ -59,6 +59,7 @@ template <int N> __device__ __forceinline__ void regs_dec() { asm volatile("setm
 __device__ __forceinline__ void st_shared16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
+__device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
 // Address of 16-byte chunk `c` (8 values) of row r in a tile of 128 rows with 128-byte swizzle.
 __device__ __forceinline__ uint32_t tile_chunk(uint32_t tile, int r, int c) {
   return tile + (uint32_t)(c >> 3) * (128 * 128) + (uint32_t)r * 128 + (uint32_t)(((c ^ r) & 7) << 4);
@@ -127,17 +128,12 @@ __device__ __forceinline__ bool find_unit(const PromptParams& p, KvSpan& span, U
   return true;
 }
 
-template <int D, bool NV>
-__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) {
+// One unit.  TWIN: at most 128 rows, which both tiles hold; tile m takes the steps k = m, m + 2, ...
+template <int D, bool NV, bool TWIN>
+__device__ __forceinline__ void run_unit(const PromptParams& p, const KvSpan& span, const Unit& u, uint8_t* smem_raw) {
   using L = PromptSmem<D>;
   constexpr int B = NV ? 16 : 32, NB = D / B;
-  extern __shared__ uint8_t smem_raw[];
   const KvAttentionLaunch& a = p.a;
-  KvSpan span;
-  Unit u;
-  grid_dep_trigger();
-  if (!find_unit<D>(p, span, u)) return;
-
   const uint32_t smem = (smem_u32(smem_raw) + 1023u) & ~1023u;
   uint8_t* base = smem_raw + (smem - smem_u32(smem_raw));
   // barriers: k_full[2], k_empty[2], v_full[2], v_empty[2], s_full[2], p_ready[2], q_ready, o_full, drain
@@ -150,7 +146,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
   uint8_t* pages_of = base + L::kBars + 128;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const bool twin = u.rows <= 128;  // both tiles hold the same rows; tile m takes the steps k = m, m + 2, ...
   if (threadIdx.x == 0) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(k_full + 8 * i, 128);
@@ -160,7 +155,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       mbar_init(s_full + 8 * i, 1);
       mbar_init(p_ready + 8 * i, 128);
     }
-    mbar_init(q_ready, twin ? 128 : 256);
+    mbar_init(q_ready, TWIN ? 128 : 256);
     mbar_init(o_full, 1);
     mbar_init(drain, 1);
     *abort_flag = 0;
@@ -181,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
     regs_inc<192>();
     const int m = warp >> 2;
     {
-      const int r = threadIdx.x & 127, row = (twin ? 0 : 128 * m) + r;
+      const int r = threadIdx.x & 127, row = (TWIN ? 0 : 128 * m) + r;
       const bool warp_live = row - lane < u.rows;  // some row of this warp exists
       const bool have = row < u.rows;
       const int at = u.row0 + (have ? row : 0);
@@ -206,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         const uint32_t q_tile = smem + L::kQ + m * L::kTile;
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
-          if (twin && m == 1) break;  // the first tile's warps store them
+          if (TWIN && m == 1) break;  // the first tile's warps store them
           uint32_t h[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j)
@@ -215,7 +210,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         }
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-      if (!twin || m == 0) mbar_arrive(q_ready);
+      if (!TWIN || m == 0) mbar_arrive(q_ready);
 
       int lo, hi;
       kv_row_range(a, span, qi, lo, hi);
@@ -225,10 +220,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       f32x2 sums[4] = {0ull, 0ull, 0ull, 0ull};
       bool ok = true;
       int turn = 0;  // steps of this tile so far
-      for (int k = twin ? m : 0; k < n; k += twin ? 2 : 1, ++turn) {
-        if (!warp_wait_short(s_full + 8 * m, turn & 1, abort_flag, p.status, 0, p.wait_ns)) { ok = false; break; }
+      for (int k = TWIN ? m : 0; k < n; k += TWIN ? 2 : 1, ++turn) {
+        if (!warp_wait(s_full + 8 * m, turn & 1, abort_flag, p.status, 0, p.wait_ns)) { ok = false; break; }
         tc_fence_after();
-        if (!warp_live) {  // rows that nobody reads
+        if (TWIN && !warp_live) {  // rows that nobody reads (in the other case the test costs 4%)
           mbar_arrive(p_ready + 8 * m);
           continue;
         }
@@ -302,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         tc_fence_before();
         mbar_arrive(p_ready + 8 * m);
       }
-      if (ok && n > 0) ok = warp_wait_short(o_full, 0, abort_flag, p.status, 1, p.wait_ns);
+      if (ok && n > 0) ok = warp_wait(o_full, 0, abort_flag, p.status, 1, p.wait_ns);
       tc_fence_after();
       float s0, s1;
       f2_unpack(f2_add(f2_add(sums[0], sums[1]), f2_add(sums[2], sums[3])), s0, s1);
@@ -311,7 +306,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       // MMA is left that reads them), and the first tile's warps add it
       const uint32_t other_o = smem + L::kK + r * 16, other_ms = smem + L::kV + r * 8;
       float f_mine = 1.0f, f_other = 0.0f;
-      if (twin) {
+      if constexpr (TWIN) {
         if (m == 1) {
           if (ok && warp_live) {
 #pragma unroll 1
@@ -336,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
           sum = sum * f_mine + sum1 * f_other;
         }
       }
-      if (ok && warp_live && !(twin && m == 1)) {
+      if (ok && warp_live && !(TWIN && m == 1)) {
         const float inv = kv_inverse(sum) * (NV ? __ldg(a.c.v_global) : 1.0f);
         const long long out_row = (span.first_q + qi) * a.q_heads + hq;
         const long long part_row = u.slot * kRows + row;
@@ -344,7 +339,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
           load_rows(t_o + c, turn > 0, o);
-          if (twin) {
+          if (TWIN) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               float x[4];
@@ -427,8 +422,25 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       }
       asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     };
-    int id = page_id(0), next_id = page_id(1);
+    // the bytes of the step after next, on their way into L2: a step is shorter than a trip to memory
+    auto prefetch = [&](int k, int id) {
+      if (id < 0 || id >= a.c.num_pages) return;
+      const int j = (u.tile0 + k) * kKeys + key;
+      const long long row = (((long long)id * a.c.heads + u.head) << a.c.page_shift) + (j & ((1 << a.c.page_shift) - 1));
+      prefetch_l2(a.c.kq + row * (D / 2));
+      prefetch_l2(a.c.vq + row * (D / 2));
+      if constexpr (D == 128) {
+        prefetch_l2(a.c.kq + row * (D / 2) + 32);
+        prefetch_l2(a.c.vq + row * (D / 2) + 32);
+      }
+      if (lane % 4 == 0) {
+        prefetch_l2(a.c.ks + row * NB);
+        prefetch_l2(a.c.vs + row * NB);
+      }
+    };
+    int id = page_id(0), next_id = page_id(1), third_id = page_id(2);
     locate(0, id);
+    prefetch(1, next_id);
     if (n > 0) {
       load(kw, ksc, a.c.kq, a.c.ks);
       load(vw, vsc, a.c.vq, a.c.vs);
@@ -436,16 +448,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
     for (int k = 0; k < n; ++k) {
       const int st = k & 1;
       const uint32_t free_parity = ((k >> 1) & 1) ^ 1;
-      if (!warp_wait_short(k_empty + 8 * st, free_parity, abort_flag, p.status, 2, p.wait_ns)) break;
+      if (!warp_wait(k_empty + 8 * st, free_parity, abort_flag, p.status, 2, p.wait_ns)) break;
       const uint32_t groups = __ballot_sync(0xFFFFFFFFu, live);
       if (lane == 0) pages_of[4 * (k & 3) + (warp & 3)] = (uint8_t)((groups & 1u) | ((groups >> 15) & 2u));
       expand(smem + L::kK + st * L::kTile, kw, ksc, false);
       mbar_arrive(k_full + 8 * st);
       // the next step's bytes are on their way while this one's values are expanded
       locate(k + 1, next_id);
-      next_id = page_id(k + 2);
+      next_id = third_id;
       if (k + 1 < n) load(kw, ksc, a.c.kq, a.c.ks);
-      if (!warp_wait_short(v_empty + 8 * st, free_parity, abort_flag, p.status, 3, p.wait_ns)) break;
+      prefetch(k + 2, third_id);
+      third_id = page_id(k + 3);
+      if (!warp_wait(v_empty + 8 * st, free_parity, abort_flag, p.status, 3, p.wait_ns)) break;
       expand(smem + L::kV + st * L::kTile, vw, vsc, true);
       mbar_arrive(v_full + 8 * st);
       if (k + 1 < n) load(vw, vsc, a.c.vq, a.c.vs);
@@ -460,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
       // scores of step k into tile m
       auto scores = [&](int m, int k) {
         if (lead) {
-          const uint32_t q = smem + L::kQ + (twin ? 0 : m) * L::kTile, kt = smem + L::kK + (k & 1) * L::kTile;
+          const uint32_t q = smem + L::kQ + (TWIN ? 0 : m) * L::kTile, kt = smem + L::kK + (k & 1) * L::kTile;
 #pragma unroll
           for (int i = 0; i < D / 16; ++i) {
             const uint32_t off = (i >> 2) * (128 * 128) + (i & 3) * 32;
@@ -478,12 +492,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
             tc_mma_f16_ts(tmem + 256 + D * m, tmem + 128 * m + 8 * i, desc_sw128_mn(vt + i * 2048, 128 * 128), i_o, !first || i > 0);
         }
       };
-      auto keys = [&](int k) { return mbar_wait_short(k_full + 8 * (k & 1), (k >> 1) & 1, abort_flag, p.status, 5, p.wait_ns); };
-      auto values = [&](int k) { return mbar_wait_short(v_full + 8 * (k & 1), (k >> 1) & 1, abort_flag, p.status, 6, p.wait_ns); };
-      auto weights = [&](int m, int turn) { return mbar_wait_short(p_ready + 8 * m, turn & 1, abort_flag, p.status, 7, p.wait_ns); };
+      auto keys = [&](int k) { return mbar_wait(k_full + 8 * (k & 1), (k >> 1) & 1, abort_flag, p.status, 5, p.wait_ns); };
+      auto values = [&](int k) { return mbar_wait(v_full + 8 * (k & 1), (k >> 1) & 1, abort_flag, p.status, 6, p.wait_ns); };
+      auto weights = [&](int m, int turn) { return mbar_wait(p_ready + 8 * m, turn & 1, abort_flag, p.status, 7, p.wait_ns); };
       auto release = [&](uint32_t bar) { if (lead) tc_commit(bar); };
       if (ok) ok = mbar_wait_short(q_ready, 0, abort_flag, p.status, 4, p.wait_ns);
-      if (twin) {
+      if constexpr (TWIN) {
         for (int k = 0; k < min(n, 2) && ok; ++k) {
           if (!keys(k)) { ok = false; break; }
           tc_fence_after();
@@ -538,6 +552,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(PromptParams p) 
   __syncthreads();
   tc_fence_after();
   if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(512));
+}
+
+template <int D, bool NV>
+__global__ void __launch_bounds__(kThreads, 1) kv_prompt_kernel(const __grid_constant__ PromptParams p) {
+  extern __shared__ uint8_t smem_raw[];
+  KvSpan span;
+  Unit u;
+  grid_dep_trigger();
+  if (!find_unit<D>(p, span, u)) return;
+  if (u.rows <= 128) run_unit<D, NV, true>(p, span, u, smem_raw);
+  else run_unit<D, NV, false>(p, span, u, smem_raw);
 }
 
 // Joins the splits of a unit: one warp a row.

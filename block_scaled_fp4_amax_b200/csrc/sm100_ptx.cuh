@@ -61,8 +61,8 @@ __device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, volatil
   return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity, abort_flag, status, site, limit));
 }
 
-// The same for waits so short that a try (which may suspend the thread for longer than they take) never
-// fails: a limit of 0 looks once, without waiting, so that giving up can be brought about.
+// The same for a wait so short that a try (which may suspend the thread for longer than it takes) hardly
+// ever fails: a limit of 0 looks once, without waiting, so that giving up can be brought about.
 __device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
   uint32_t ok;
   asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
@@ -78,11 +78,6 @@ __device__ __forceinline__ bool mbar_wait_short(uint32_t bar, uint32_t parity, v
   *abort_flag = 1;
   return false;
 }
-__device__ __forceinline__ bool warp_wait_short(uint32_t bar, uint32_t parity, volatile int* abort_flag, uint32_t* status,
-                                                uint32_t site, unsigned long long limit) {
-  return __all_sync(0xFFFFFFFFu, mbar_wait_short(bar, parity, abort_flag, status, site, limit));
-}
-
 // Drain wait (exit paths): until the phase completes or kTimeoutNs passes, whatever the flags say.
 __device__ __forceinline__ void mbar_drain(uint32_t bar, uint32_t parity) {
   const unsigned long long t0 = now_ns();
