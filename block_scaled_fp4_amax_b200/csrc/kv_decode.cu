@@ -56,6 +56,7 @@ struct DecodeParams {
   float2* part_ml; // their maximum and sum, [slot][row]
   KvJoin* joins;   // one per unit, or, where there are more units than CTAs, one per CTA
   bool by_unit;
+  bool whole;      // units are not cut: a CTA takes those whose first tile falls into its share
   uint32_t* status;
 };
 
@@ -118,7 +119,14 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   const long long total = sched.prefix[nseq] * a.c.heads;
   const int cta = blockIdx.x;
   const long long n = min((long long)gridDim.x, total);  // every CTA that works has a tile
-  const long long x0 = cta < n ? cta * total / n : 0, x1 = cta < n ? (cta + 1) * total / n : 0;
+  long long x0 = cta < n ? cta * total / n : 0, x1 = cta < n ? (cta + 1) * total / n : 0;
+  if (p.whole) {
+    KvCursor c;
+    kv_seek<kTile>(a, c, sched, seq0, nseq, x0);
+    if (c.tile > 0) x0 += c.tiles - c.tile;
+    kv_seek<kTile>(a, c, sched, seq0, nseq, x1);
+    if (c.tile > 0) x1 += c.tiles - c.tile;
+  }
   KvJoin join = {0, 0, 0, 0, 0, 0};
 
   // The cursor that fills the ring runs ahead of the one that consumes it, across units.
@@ -316,17 +324,21 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       // ---- mask: only where some row's range ends inside the tokens, or a page is missing
       const int j0 = (use.first + tile) * kTile + mine;
       if ((gone & ((1u << kGroups) - 1u)) != 0u || j0 < span.lo_all || j0 + kWarpTokens > span.hi_all) {
+        const bool one = span.queries == 1;  // then every row has the same range
 #pragma unroll
-        for (int h2 = 0; h2 < kGroups; ++h2)
+        for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
+          for (int c = 0; c < 2; ++c) {
+            int lo = span.lo_all, hi = span.hi_all;
+            if (!one) kv_row_range(a, span, (8 * nt + 2 * t + c) / p.group, lo, hi);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int r = 8 * nt + 2 * t + (c & 1), j = j0 + 16 * h2 + tok + (c >= 2 ? 8 : 0);
-              int lo, hi;
-              kv_row_range(a, span, r / p.group, lo, hi);
-              if (((gone >> h2) & 1u) || j < lo || j >= hi) s[h2][nt][c] = -INFINITY;
-            }
+            for (int h2 = 0; h2 < kGroups; ++h2)
+#pragma unroll
+              for (int u = 0; u < 2; ++u) {
+                const int j = j0 + 16 * h2 + tok + 8 * u;
+                if (((gone >> h2) & 1u) || j < lo || j >= hi) s[h2][nt][c + 2 * u] = -INFINITY;
+              }
+          }
       }
 
       // ---- running maximum (raised rarely), weights, sums
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       const long long last = (end * n - 1) / total;   // the CTA that owns tile end - 1
       join = {(int)(last - cta + 1), rows, head, (int)(slot & 1), span.first_q, blockIdx.y * gridDim.x + cta};
     }
-    if (p.by_unit && tile0 == 0 && threadIdx.x == 0) {
+    if (p.by_unit && !p.whole && tile0 == 0 && threadIdx.x == 0) {
       p.joins[(long long)seq * a.c.heads + head] = join;
       join.parts = 0;
     }
@@ -479,7 +491,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
     use.tile = tile1;
     if (use.tile == use.tiles) kv_next<kTile>(a, use, sched, seq0, nseq);
   }
-  if (!p.by_unit && threadIdx.x == 0) p.joins[blockIdx.y * gridDim.x + cta] = join;
+  if (!p.by_unit && !p.whole && threadIdx.x == 0) p.joins[blockIdx.y * gridDim.x + cta] = join;
 }
 
 // Joins the parts of a unit: part 0 lies in the slot `join.slot` of the CTA that began the unit, the others
@@ -581,6 +593,12 @@ cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
   p.status = reinterpret_cast<uint32_t*>(ws);
   ws += kKvStatusBytes;
   p.joins = reinterpret_cast<KvJoin*>(ws);
+  // Short tables: a unit's few tiles one after another cost less than the joining launch where units fill the
+  // SMs (512 units of 300, 1024 and 2048 tokens: 25, 33 and 40 us cut, 17, 29 and 43 us whole; 64
+  // units of 1024: 12 and 16 us); up to three tiles they cost as much, and a launch less (8 units of
+  // 300: 7.7 us either way).
+  const int span = p.a.max_pages << p.a.c.page_shift;
+  p.whole = span <= 3 * kTile || (span <= 8 * kTile && (long long)p.a.seqs * p.a.c.heads >= 2 * num_sms());
   p.by_unit = (long long)p.a.seqs * p.a.c.heads <= n * chunks;
   ws += (size_t)num_sms() * kMaxCtasPerSm * sizeof(KvJoin);
   p.part_ml = reinterpret_cast<float2*>(ws);
@@ -591,6 +609,7 @@ cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
   if (e != cudaSuccess) return e;
   kv_decode_kernel<D, NV, NT><<<dim3(n, chunks), 32 * kWarps, smem, s>>>(p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  if (p.whole) return cudaSuccess;
   // A block per unit where there are fewer units than CTAs (a grid of 592 blocks that find nothing to do
   // costs 2 us); for few units more threads and blocks each.
   constexpr int passes = 8 * NT * (D / 4) / 128;

@@ -661,7 +661,9 @@ cudaError_t launch_kv_prompt(const KvAttentionLaunch& L, cudaStream_t s) {
   p.a = L;
   p.group = L.q_heads / L.c.heads;
   p.qtiles = (int)(((long long)L.max_q * p.group + kRows - 1) / kRows);
-  // Few units: the keys of each are split over the SMs that would be idle, four steps of 128 at least.
+  // Few units: the keys of each are split over the SMs that would be idle, four steps of 128 at least (48
+  // queries over 60000 tokens, 32/8 heads: 829 us in 8 CTAs, 81 us in 144; 64 over 8192, 64/8 heads: 127
+  // and 42 us).
   const long long units = kv_prompt_units(L);
   const long long steps = (((long long)L.max_pages << L.c.page_shift) + kKeys - 1) / kKeys;
   p.splits = 1;

@@ -375,7 +375,7 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  *   and the key has a page.  A query that sees no key gives zeros and lse = -inf.
  * Scores, softmax statistics and sums are fp32; keys and values enter the products exactly, the
  * queries too (scaled per row by a power of two), and the softmax weights, fp32 in the sum that
- * divides, are rounded to fp16 (2^-12 of each weight) for the product with V.  A query row holding
+ * divides, are rounded to fp16 (off by 2^-11 of a weight at most) for the product with V.  A query row holding
  * Inf or NaN is unspecified; an MXFP4 scale byte outside 104 .. 140 counts as the nearest of these;
  * an E4M3 NaN scale byte of a key gives NaN in the rows that see it, one of a value block counts as 0
  * (a product with a weight of 0 would carry it into rows that do not see the token).
@@ -391,7 +391,7 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  *   Limits: total_q <= 2^24, seqs <= 32768, max_pages * page_size <= 2^30, q_heads <= 4096.
  *   lse   : device float [total_q, q_heads] or NULL: natural log of the sum of exp(scale q k).
  *   workspace : device, 16-byte aligned, >= fp4_workspace_size(FP4_OP_KV_ATTENTION, total_q, q_heads)
- *           bytes; clobbered, needs no initialisation.  Calls that overlap need one each.  Its first 4
+ *           bytes (asked with the call's device current); clobbered, needs no initialisation.  Calls that overlap need one each.  Its first 4
  *           bytes are a status word, 0 when every pipeline wait of the call ended; otherwise bit i
  *           names the wait that gave up (many rows only: 0 scores, 1 the output, 2 and 3 a free key
  *           and value stage, 4 the queries, 5 and 6 a full key and value stage, 7 weights) and the

@@ -163,6 +163,15 @@ def test_read_missing_pages_and_ranges(cuda):
     assert np.array_equal(kk[seen], want.cpu().numpy()[t[seen]])
 
 
+def test_read_many_sequences(cuda):
+    """More sequences than a block keeps offsets of, empty ones among them."""
+    lens = [(7 * i) % 5 for i in range(1500)]
+    c = Cache(lens, 1, 64, 16, fp4.MXFP4, seed=1)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(lens)]), dtype=torch.int32, device=cuda)
+    k, v = fp4.fp4_kv_read(c.arrays, c.table, cu, sum(lens), fp4.MXFP4, out_dtype=torch.float32)
+    assert np.array_equal(k.cpu().numpy(), np.concatenate(c.k64)) and np.array_equal(v.cpu().numpy(), np.concatenate(c.v64))
+
+
 # ---------------------------------------------------------------------------------------------
 # attention
 
@@ -427,7 +436,7 @@ def test_sequences_without_queries_or_keys(cuda, queries):
     run_and_check(c, [0, 0, 0, queries, 0, 0], 4)
 
 
-@pytest.mark.parametrize("seqs,heads,long", [(90, 8, 3000), (300, 2, 700), (600, 1, 90)])
+@pytest.mark.parametrize("seqs,heads,long", [(90, 8, 3000), (300, 2, 700), (300, 1, 2000), (600, 1, 90)])
 def test_many_sequences(cuda, seqs, heads, long):
     """More units than resident blocks, and more sequences than one schedule holds."""
     lens = [long] + [(37 * i) % 60 for i in range(1, seqs)]

@@ -55,6 +55,7 @@ def attend(L, **kw):
     (dict(fmt=2), EUNSUPPORTED), (dict(fmt=5), EINVAL), (dict(block=32), EINVAL), (dict(fmt=0, block=16), EINVAL),
     (dict(dim=96), EUNSUPPORTED), (dict(dim=256), EUNSUPPORTED), (dict(page=8), EINVAL), (dict(page=48), EINVAL),
     (dict(page=2048), EINVAL), (dict(heads=0), EINVAL), (dict(heads=1025, hq=1025), EINVAL), (dict(pages=0), EINVAL), (dict(pages=2 ** 31), EINVAL),
+    (dict(pages=2 ** 30, page=1024, heads=64, hq=64), EUNSUPPORTED),
     (dict(kq=None), EINVAL), (dict(vs=None), EINVAL), (dict(ks=ODD), EINVAL), (dict(kg=None), EINVAL), (dict(vg=None), EINVAL)])
 def test_cache_refusals(L, call, kw, status):
     if call is not attend:
@@ -84,7 +85,9 @@ def test_read_refusals(L, kw):
     (dict(total=2 ** 25), EINVAL), (dict(total=4), EINVAL), (dict(max_q=0), EINVAL), (dict(scale=float("nan")), EINVAL),
     (dict(scale=float("inf")), EINVAL), (dict(window=-1), EINVAL), (dict(q=None), EINVAL), (dict(q=ODD), EINVAL),
     (dict(qs=1020), EINVAL), (dict(qh=-128), EINVAL), (dict(lens=None), EINVAL), (dict(out=None), EINVAL), (dict(out=ODD), EINVAL),
-    (dict(ws=None), EINVAL), (dict(ws=ODD), EINVAL), (dict(ws_bytes=0), EINVAL), (dict(table=None), EINVAL), (dict(stride=1), EINVAL)])
+    (dict(seqs=40000, total=40000), EUNSUPPORTED),
+    (dict(page=1024, cols=2 ** 21, stride=2 ** 21), EUNSUPPORTED), (dict(cu=FAKE, max_q=2 ** 30), EUNSUPPORTED),
+    (dict(cu=FAKE, max_q=2 ** 28, heads=1, hq=1, seqs=3000, total=2 ** 24), EUNSUPPORTED), (dict(ws=None), EINVAL), (dict(ws=ODD), EINVAL), (dict(ws_bytes=0), EINVAL), (dict(table=None), EINVAL), (dict(stride=1), EINVAL)])
 def test_attention_refusals(L, kw, status):
     assert attend(L, **kw) == status
 
