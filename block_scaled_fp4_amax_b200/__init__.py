@@ -385,7 +385,7 @@ def fp4_kv_read(cache, table: torch.Tensor, cu: torch.Tensor, total: int, fmt: i
     """Dequantise ranges of the cache: rows cu[b]..cu[b+1]-1 of the outputs are tokens starts[b].. (0..
     without `starts`) of sequence b.  cu: int32 [seqs + 1]; total: rows of the outputs, cu[-1] for
     the caller that knows it.  Returns (k, v) [total, heads, head_dim] in out_dtype, or fills
-    `out` = (k, v) (rows from cu[-1] on are left as they were)."""
+    `out` = (k, v) (rows from cu[-1] on are left as they were, unset in new ones)."""
     if out is None:
         out = (None, None)
         if out_dtype is not torch.bfloat16 and out_dtype is not torch.float32:
@@ -398,17 +398,22 @@ def fp4_kv_read(cache, table: torch.Tensor, cu: torch.Tensor, total: int, fmt: i
 
 
 def fp4_kv_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Tensor, fmt: int = NVFP4,
-                     cu_q: torch.Tensor | None = None, max_q: int = 1, scale: float | None = None,
+                     cu_q: torch.Tensor | None = None, max_q: int | None = None, scale: float | None = None,
                      causal: bool = True, window: int = 0, want_lse: bool = False,
                      k_global: torch.Tensor | None = None, v_global: torch.Tensor | None = None,
                      out: torch.Tensor | None = None, stream=None, workspace: torch.Tensor | None = None):
     """Attention of bf16 queries q [total_q, q_heads, head_dim] (any token and head strides) over the
     cache.  Query head h reads key/value head h // (q_heads // heads); the queries of a sequence are
     its last tokens.  lens: int32 [seqs], keys of each sequence; cu_q: int32 [seqs + 1], queries
-    cu_q[b]..cu_q[b+1]-1 belong to sequence b, at most max_q each (without it, max_q for every
-    sequence); scale: 1 / sqrt(head_dim) by default; window: keys a query sees, itself the last one (0:
+    cu_q[b]..cu_q[b+1]-1 belong to sequence b, at most max_q each (queries past max_q are not computed;
+    without cu_q every sequence has max_q, 1 by default); scale: 1 / sqrt(head_dim) by default; window: keys a query sees, itself the last one (0:
     all).  Returns (out bf16 [total_q, q_heads, head_dim], lse float32 [total_q, q_heads] or None);
-    a query that sees no key gives zeros and lse = -inf."""
+    a query that sees no key gives zeros and lse = -inf; rows of no sequence (from cu_q[-1] on) keep what
+    `out` held, unset in a new one.  For inference: no gradients."""
+    if max_q is None:
+        if cu_q is not None:
+            raise ValueError("max_q (the largest number of queries of a sequence) is needed with cu_q")
+        max_q = 1
     r = (_kv or _kv_native()).kv_attention(q, *cache, table, lens, fmt, cu_q, max_q, q.shape[-1] ** -0.5 if scale is None else scale,
                                            causal, window, want_lse, k_global, v_global, out, workspace, _kv_stream(stream))
     if type(r) is int:

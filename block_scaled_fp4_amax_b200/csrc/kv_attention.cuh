@@ -176,6 +176,12 @@ __device__ __forceinline__ void kv_schedule(const KvAttentionLaunch& a, int seq0
   }
 }
 
+// a / b (a >= 0, b > 0), in 32 bits where both fit, which is nearly always and several times shorter.
+__device__ __forceinline__ long long kv_div(long long a, long long b) {
+  if (((unsigned long long)(a | b) >> 32) == 0) return (long long)((uint32_t)a / (uint32_t)b);
+  return a / b;
+}
+
 // The unit and tile of linear index x (0 <= x < heads * prefix[nseq]); past the end an empty cursor.
 template <int TILE>
 __device__ __forceinline__ void kv_seek(const KvAttentionLaunch& a, KvCursor& c, const KvSchedule& sc, int seq0, int nseq,
@@ -193,7 +199,7 @@ __device__ __forceinline__ void kv_seek(const KvAttentionLaunch& a, KvCursor& c,
   c.seq = lo;
   c.tiles = (int)(sc.prefix[lo + 1] - sc.prefix[lo]);
   const long long rest = x - sc.prefix[lo] * heads;
-  c.head = (int)(rest / c.tiles);
+  c.head = (int)kv_div(rest, c.tiles);
   c.tile = (int)(rest - (long long)c.head * c.tiles);
   kv_tiles<TILE>(kv_span(a, seq0 + lo), c.first);
 }

@@ -113,13 +113,14 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   float* coef_shared = merge + NT * 32 * (D / 8);
 
   grid_dep_trigger();
+  const float gk = NV ? __ldg(a.c.k_global) : 1.0f, gv = NV ? __ldg(a.c.v_global) : 1.0f;  // on their way early
   if (blockIdx.x == 0 && blockIdx.y == 0 && threadIdx.x == 0) *p.status = 0u;  // no wait here can give up
   const int seq0 = blockIdx.y * p.chunk_seqs, nseq = min(p.chunk_seqs, a.seqs - seq0);
   kv_schedule<kTile, 32 * kWarps>(a, seq0, nseq, sched);
   const long long total = sched.prefix[nseq] * a.c.heads;
   const int cta = blockIdx.x;
   const long long n = min((long long)gridDim.x, total);  // every CTA that works has a tile
-  long long x0 = cta < n ? cta * total / n : 0, x1 = cta < n ? (cta + 1) * total / n : 0;
+  long long x0 = cta < n ? kv_div(cta * total, n) : 0, x1 = cta < n ? kv_div((cta + 1) * total, n) : 0;
   if (p.whole) {
     KvCursor c;
     kv_seek<kTile>(a, c, sched, seq0, nseq, x0);
@@ -187,6 +188,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
     const int seq = seq0 + use.seq, head = use.head;
     const KvSpan span = kv_span(a, seq);
     const int rows = span.queries * p.group;
+    const bool one = span.queries == 1;  // then row r is query head r, and every row sees the same keys
     const int tile0 = use.tile;
     const int tile1 = (int)min((long long)use.tiles, tile0 + (x1 - x));
 
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       uint32_t raw[D / 8];
       uint32_t m = 0u;
       const bool have = r < rows;
-      const int qi = have ? r / p.group : 0;
+      const int qi = have && !one ? r / p.group : 0;
       const char* src = reinterpret_cast<const char*>(a.q) +
                         2 * ((span.first_q + qi) * a.q_stride + (long long)(head * p.group + (have ? r - qi * p.group : 0)) * a.q_head_stride + t * (D / 4));
 #pragma unroll
@@ -216,7 +218,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       float up, down;
       kv_query_scale(m, up, down);
-      float c = a.scale * 1.44269504f * (NV ? __ldg(a.c.k_global) : 1.0f) * down;
+      float c = a.scale * 1.44269504f * gk * down;
       kv_positive(c, up);
       coef[k] = c;
 #pragma unroll
@@ -324,7 +326,6 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       // ---- mask: only where some row's range ends inside the tokens, or a page is missing
       const int j0 = (use.first + tile) * kTile + mine;
       if ((gone & ((1u << kGroups) - 1u)) != 0u || j0 < span.lo_all || j0 + kWarpTokens > span.hi_all) {
-        const bool one = span.queries == 1;  // then every row has the same range
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -447,7 +448,6 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
     const bool part = head_part || tail_part;
     // a CTA's first part goes to slot 0, a later one (the last unit's) to slot 1
     const long long slot = 2LL * (blockIdx.y * gridDim.x + cta) + (x == x0 ? 0 : 1);
-    const float gv = NV ? __ldg(a.c.v_global) : 1.0f;
     constexpr int PAIRS = D / 2;
     for (int i = threadIdx.x; i < rows * PAIRS; i += 32 * kWarps) {
       const int r = i / PAIRS, d2 = i % PAIRS;  // channels 2 d2, 2 d2 + 1
@@ -469,7 +469,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
         *reinterpret_cast<float2*>(p.part + (slot * 8 * NT + r) * D + 2 * d2) = make_float2(v0, v1);
         if (d2 == 0) p.part_ml[slot * 8 * NT + r] = make_float2(m, l);
       } else {
-        const int qi = r / p.group;
+        const int qi = one ? 0 : r / p.group;
         const long long row = (span.first_q + qi) * a.q_heads + head * p.group + (r - qi * p.group);
         const float inv = kv_inverse(l) * gv;
         reinterpret_cast<uint32_t*>(a.out)[row * PAIRS + d2] = bf16x2_pack(v0 * inv, v1 * inv);
@@ -479,7 +479,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
     if (tail_part && !head_part) {
       // this CTA holds the unit's first part: how many CTAs hold the rest, for the joining launch
       const long long end = x + (use.tiles - tile0);  // one past the unit's last tile
-      const long long last = (end * n - 1) / total;   // the CTA that owns tile end - 1
+      const long long last = kv_div(end * n - 1, total);   // the CTA that owns tile end - 1
       join = {(int)(last - cta + 1), rows, head, (int)(slot & 1), span.first_q, blockIdx.y * gridDim.x + cta};
     }
     if (p.by_unit && !p.whole && tile0 == 0 && threadIdx.x == 0) {

@@ -563,7 +563,8 @@ def test_binding_refusals(cuda):
     for err, kw in [(TypeError, dict(q=q.half())), (fp4.Fp4Error, dict(q=q.float())), (ValueError, dict(q=q[..., :32])),
                     (ValueError, dict(q=q.cpu())), (ValueError, dict(q=q.expand(2, 1, 4, 64))), (fp4.Fp4Error, dict(q=q[:, :3])),
                     (ValueError, dict(table=c.table.long())), (ValueError, dict(table=c.table[:, ::2])), (ValueError, dict(lens=c.lens_t.cpu())),
-                    (ValueError, dict(lens=c.lens_t.long())), (ValueError, dict(cu_q=c.lens_t)), (fp4.Fp4Error, dict(max_q=2)),
+                    (ValueError, dict(lens=c.lens_t.long())), (ValueError, dict(cu_q=c.lens_t, max_q=1)),
+                    (ValueError, dict(cu_q=torch.tensor([0, 1], dtype=torch.int32, device=cuda))), (fp4.Fp4Error, dict(max_q=2)),
                     (fp4.Fp4Error, dict(scale=float("nan"))), (ValueError, dict(out=torch.empty_like(q).float())),
                     (fp4.Fp4Error, dict(workspace=torch.empty(16, dtype=torch.uint8, device=cuda))), (fp4.Fp4Error, dict(k_global=None)),
                     (ValueError, dict(k_global=torch.ones(2, device=cuda))), (ValueError, dict(cache=c.arrays[:3] + (c.arrays[3][:1],))),
