@@ -11,8 +11,9 @@ namespace fp4k {
 // (exp2(-inf - max)) are zeros and never NaN.
 constexpr float kNoMax = -3e38f;
 // The running maximum is raised when a score passes it by more than kRaise (in log2 units), and
-// weights carry a factor 2^kShift: they stay at or below 2^15, inside fp16, and a weight of 2^-29 of
-// the largest possible one is still a normal fp16 number.
+// weights carry a factor 2^kShift: they stay at or below 2^15, inside fp16.  The largest weight of a row is
+// at least 2^kShift (the maximum never exceeds the row's), so a weight of 2^-21 of it is still a normal
+// fp16 number; smaller ones are off by half a step of the subnormals, 2^-25: 2^-32 of the largest.
 constexpr float kRaise = 8.0f, kShift = 7.0f;
 
 __device__ __forceinline__ float exp2_approx(float x) {

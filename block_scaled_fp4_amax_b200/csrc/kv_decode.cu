@@ -19,8 +19,8 @@
 // Values v * d (E2M1 times block scale) are exact in fp16; the per-tensor scales act on the fp32 sums.
 // Queries are scaled per row by a power of two so that fp16 holds their bf16 values exactly.  Weights
 // exp2(z - m + 7) are rounded to fp16 for the product (m is the running maximum; it is raised only
-// when a score passes it by 8, so weights stay below 2^15 and 2^-29 of the largest keeps full
-// precision) and summed unrounded.
+// when a score passes it by 8, so weights stay below 2^15, and those of 2^-21 of a row's largest keep
+// full precision) and summed unrounded.
 #include "fp4_device.cuh"
 #include "kv_attention.cuh"
 #include "launch.h"

@@ -375,7 +375,8 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  *   and the key has a page.  A query that sees no key gives zeros and lse = -inf.
  * Scores, softmax statistics and sums are fp32; keys and values enter the products exactly, the
  * queries too (scaled per row by a power of two), and the softmax weights, fp32 in the sum that
- * divides, are rounded to fp16 (off by 2^-11 of a weight at most) for the product with V.  A query row holding
+ * divides, are rounded to fp16 for the product with V: off by 2^-11 of a weight, or by 2^-32 of the
+ * row's largest weight where that is more.  A query row holding
  * Inf or NaN is unspecified; an MXFP4 scale byte outside 104 .. 140 counts as the nearest of these;
  * an E4M3 NaN scale byte of a key gives NaN in the rows that see it, one of a value block counts as 0
  * (a product with a weight of 0 would carry it into rows that do not see the token).

@@ -113,13 +113,15 @@ def check(out, lse, ref, n, dim, vmax):
     """The error a row may have, from the roundings the documentation names.
     Scores: dim products summed in fp32, each partial sum off by 2^-23 of the sum of magnitudes
     (tensor cores may truncate), and a few further roundings: ds = (dim + 8) 2^-23 sum |q k| scale.
-    Weights: e^ds, 2^-11 from fp16, 2^-22 from the exponential; weights below 2^-29 of the largest
-    lose relative precision, an absolute 2^-38.  Sums over n keys: (n + 16) 2^-23.  Output: bf16, 2^-8."""
+    Weights: e^ds, 2^-11 from fp16, 2^-22 from the exponential.  A row's largest weight is written as at
+    least 2^7, so a weight below 2^-21 of it is an fp16 subnormal, off by half their step: 2^-24 / 2 /
+    2^7 = 2^-32 of the largest, which is at most the sum of all: n 2^-32 of the largest |v| for n
+    keys.  Sums over n keys: (n + 16) 2^-23.  Output: bf16, 2^-8."""
     o64, l64, A, sabs = ref
     ds = (dim + 8) * 2.0 ** -23 * sabs
     o = out.float().cpu().numpy().astype(np.float64)
     bound = 2.0 ** -8 * np.abs(o64) + A * (2.0 ** -11 + 2 * ds[..., None] + (n + 16) * 2.0 ** -23) * (1 + 2.0 ** -8) \
-        + n * 2.0 ** -38 * vmax
+        + n * 2.0 ** -32 * vmax
     err = np.abs(o - o64)
     assert np.isfinite(o).all()
     assert (err <= bound).all(), f"{(err > bound).sum()} of {err.size} outside; worst ratio {np.nanmax(err / np.maximum(bound, 1e-300)):.3f}"
