@@ -409,7 +409,9 @@ def fp4_kv_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Te
     without cu_q every sequence has max_q, 1 by default); scale: 1 / sqrt(head_dim) by default; window: keys a query sees, itself the last one (0:
     all).  Returns (out bf16 [total_q, q_heads, head_dim], lse float32 [total_q, q_heads] or None);
     a query that sees no key gives zeros and lse = -inf; rows of no sequence (from cu_q[-1] on) keep what
-    `out` held, unset in a new one.  For inference: no gradients."""
+    `out` held, unset in a new one.  Rows of a pipeline wait that gave up are NaN (and named in the status
+    word, the first 4 bytes of `workspace`, uint8 [workspace_size(OP_KV_ATTENTION)], where the caller
+    keeps one).  For inference: no gradients."""
     if max_q is None:
         if cu_q is not None:
             raise ValueError("max_q (the largest number of queries of a sequence) is needed with cu_q")

@@ -341,15 +341,18 @@ __device__ __forceinline__ void run_unit(const PromptParams& p, const KvSpan& sp
           sum = sum * f_mine + sum1 * f_other;
         }
       }
-      if (ok && warp_live && !(TWIN && m == 1)) {
+      // A warp whose wait gave up writes NaN rows: its weights or sums are incomplete, and a caller without a
+      // workspace of its own has no status word to read.  (In a split unit the sum carries the NaN through the join.)
+      if (!ok) sum = __uint_as_float(0x7FC00000u);
+      if (warp_live && !(TWIN && m == 1)) {
         const float inv = kv_inverse(sum) * (NV ? __ldg(a.c.v_global) : 1.0f);
         const long long out_row = (span.first_q + qi) * a.q_heads + hq;
         const long long part_row = u.slot * kRows + row;
 #pragma unroll 1
         for (int c = 0; c < D; c += 32) {
           uint32_t o[32];
-          load_rows(t_o + c, turn > 0, o);
-          if (TWIN) {
+          load_rows(t_o + c, ok && turn > 0, o);
+          if (TWIN && ok) {
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               float x[4];

@@ -395,8 +395,10 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  *           bytes (asked with the call's device current); clobbered, needs no initialisation.  Calls that overlap need one each.  Its first 4
  *           bytes are a status word, 0 when every pipeline wait of the call ended; otherwise bit i
  *           names the wait that gave up (many rows only: 0 scores, 1 the output, 2 and 3 a free key
- *           and value stage, 4 the queries, 5 and 6 a full key and value stage, 7 weights) and the
- *           output is incomplete.  The limit is that of fp4_set_gemm_wait_limit.
+ *           and value stage, 4 the queries, 5 and 6 a full key and value stage, 7 weights), and the
+ *           rows of out and lse whose work was cut short are NaN, so that a caller who cannot read
+ *           the word sees it too.  The limit is that of fp4_set_gemm_wait_limit.  A call without
+ *           queries or sequences launches nothing and leaves the word.
  * No gradients: a cache in 4 bits serves inference. */
 FP4_API fp4_status fp4_kv_attention(const void* q, fp4_dtype dtype, long total_q, long q_stride,
                                     long q_head_stride, int q_heads, const unsigned char* kq,

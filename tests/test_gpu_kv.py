@@ -587,3 +587,31 @@ def test_binding_refusals(cuda):
         a.update(kw)
         with pytest.raises(err):
             fp4.fp4_kv_read(c.arrays, c.table, a.pop("cu"), 40, **a, **c.scales)
+
+
+# Rows, steps and units of the many-row kernel: two row tiles or one, keys split over blocks or not.
+@pytest.mark.parametrize("queries,length", [(300, 700), (300, 6000), (20, 700), (20, 6000)])
+def test_a_lost_wait_shows_in_the_output(cuda, queries, length):
+    """Without a workspace of the caller's nobody can read the status word: rows of a block that gave up are
+    NaN, all others right.  With one, its status word says so, and the next call on it is right."""
+    c = Cache([length], 1, 128, 16, fp4.NVFP4)
+    q = torch.randn(queries, 4, 128, device=cuda).to(torch.bfloat16)
+    call = lambda **kw: fp4.fp4_kv_attention(q, c.arrays, c.table, c.lens_t, max_q=queries, want_lse=True, **kw, **c.scales)  # noqa: E731
+    want, want_lse = call()
+    ws = torch.zeros(fp4.workspace_size(fp4.OP_KV_ATTENTION), dtype=torch.uint8, device=cuda)
+    got = []
+    torch.cuda.synchronize()
+    old = fp4.set_gemm_wait_limit(0)
+    try:
+        for kw in (dict(), dict(workspace=ws)):
+            got.append(call(out=torch.full_like(want, 7.0), **kw))
+            torch.cuda.synchronize()
+    finally:
+        fp4.set_gemm_wait_limit(old)
+    assert int(ws[:4].view(torch.int32)) != 0
+    for out, lse in got:
+        right = (out == want).all(-1) & (lse == want_lse)
+        lost = out.isnan().all(-1) & lse.isnan()
+        assert bool(lost.any()) and bool((right | lost).all())
+    run_and_check(c, [queries], 4, workspace=ws)
+    assert int(ws[:4].view(torch.int32)) == 0
