@@ -39,7 +39,7 @@ fp4_status check_cache(const unsigned char* kq, const unsigned char* ks, const u
   if (head_dim != 64 && head_dim != 128) return kv_fail(FP4_EUNSUPPORTED, "head_dim %d: 64 and 128 are supported", head_dim);
   if (page_size < 16 || page_size > 1024 || (page_size & (page_size - 1)))
     return kv_fail(FP4_EINVAL, "page_size %d must be a power of two in 16 .. 1024", page_size);
-  if (heads < 1 || heads > 1024) return kv_fail(FP4_EINVAL, "heads %d outside 1 .. 1024", heads);
+  if (heads < 1 || heads > fp4k::kKvMaxHeads) return kv_fail(FP4_EINVAL, "heads %d outside 1 .. %d", heads, fp4k::kKvMaxHeads);
   if (num_pages < 1 || num_pages >= (1L << 31)) return kv_fail(FP4_EINVAL, "num_pages %ld outside 1 .. 2^31 - 1", num_pages);
   if (((long long)num_pages * page_size >> 4) * heads >= (1LL << 31))
     return kv_fail(FP4_EUNSUPPORTED, "a cache of 2^35 rows or more");
@@ -144,7 +144,7 @@ fp4_status fp4_kv_attention(const void* q, fp4_dtype dtype, long total_q, long q
   if (total_q < 0 || total_q > (1L << 24)) return kv_fail(FP4_EINVAL, "total_q %ld outside 0 .. 2^24", total_q);
   if (!std::isfinite(scale)) return kv_fail(FP4_EINVAL, "scale must be finite");
   if (seqs > 32768) return kv_fail(FP4_EUNSUPPORTED, "seqs %d above 32768", seqs);
-  if ((long long)max_pages * page_size > (1LL << 30))
+  if ((long long)max_pages * page_size > fp4k::kKvMaxTokens)
     return kv_fail(FP4_EUNSUPPORTED, "a block table of more than 2^30 tokens a sequence");
   if (window < 0) return kv_fail(FP4_EINVAL, "window %d is negative (0: no window)", window);
   if (total_q == 0 || seqs == 0) return FP4_OK;

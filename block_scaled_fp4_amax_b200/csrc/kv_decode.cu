@@ -136,7 +136,9 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
   use = fill;
   constexpr int kRow = D / 2;  // nibble bytes of a token
   const int mine = kWarpTokens * warp;  // of a tile's tokens
-  int left = (int)(x1 - x0);   // tiles still to fetch
+  long long left = x1 - x0;    // tiles still to fetch
+  static_assert(kKvMaxTokens / kTile * kMaxSchedSeqs * kKvMaxHeads < 1LL << (8 * sizeof(left) - 2),
+                "a CTA's share of the largest call");
   // Where this warp's groups of the next 16 tiles of the unit lie, one group a lane: the cache's rows in
   // groups of 16 (they fit 32 bits), -1 without a page.
   int places = -1, places_tile = -1;

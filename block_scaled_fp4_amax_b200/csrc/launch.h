@@ -96,6 +96,10 @@ struct GemmLaunch {
   uint32_t* status;  // device status word
 };
 
+// Limits of the cache's calls: key/value heads, and tokens that a block table spans.
+constexpr int kKvMaxHeads = 1024;
+constexpr long long kKvMaxTokens = 1LL << 30;
+
 // The paged 4-bit key/value cache: nibbles [num_pages, heads, page, head_dim / 2] and scale bytes
 // [num_pages, heads, page, head_dim / block] for the keys and for the values.
 struct KvCache {
