@@ -615,3 +615,20 @@ def test_a_lost_wait_shows_in_the_output(cuda, queries, length):
         assert bool(lost.any()) and bool((right | lost).all())
     run_and_check(c, [queries], 4, workspace=ws)
     assert int(ws[:4].view(torch.int32)) == 0
+
+
+@pytest.mark.parametrize("group", [2, 12, 20, 32])
+def test_units_cut_in_two_schedules(cuda, group):
+    """More than 256 sequences, more units than blocks and a wide table: long units at both ends of both
+    schedules are cut, and joined from the records of each block."""
+    lens = [(37 * i) % 60 for i in range(300)]
+    for b in (0, 75, 149, 150, 220, 299):
+        lens[b] = 2500 - 3 * b
+    c = Cache(lens, 3, 64, 16, fp4.MXFP4, seed=4)
+    run_and_check(c, [1] * 300, group)
+
+
+@pytest.mark.parametrize("queries", [1, 40])
+def test_many_heads(cuda, queries):
+    c = Cache([150, 20, 0], 40, 64, 16, fp4.NVFP4, seed=6)
+    run_and_check(c, [queries] * 3, 1, strided=True)
