@@ -51,7 +51,8 @@ __device__ __forceinline__ uint32_t kv_scale_f16x2(uint32_t byte) {
   return f16x2_pack(s, s);
 }
 // The scales of two value blocks.  A NaN byte counts as 0: its product with a weight of 0 would reach
-// rows that do not see the token (max returns the operand that is a number).
+// rows that do not see the token (max returns the operand that is a number).  A negative scale, which no
+// block is written with, counts as 0 by the same instruction.
 template <bool NV>
 __device__ __forceinline__ uint32_t kv_value_scales(uint32_t b0, uint32_t b1) {
   if constexpr (NV) {

@@ -379,7 +379,9 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  * row's largest weight where that is more.  A query row holding
  * Inf or NaN is unspecified; an MXFP4 scale byte outside 104 .. 140 counts as the nearest of these;
  * an E4M3 NaN scale byte of a key gives NaN in the rows that see it, one of a value block counts as 0
- * (a product with a weight of 0 would carry it into rows that do not see the token).
+ * (a product with a weight of 0 would carry it into rows that do not see the token), and so does a
+ * value block's byte with its sign bit set, which fp4_kv_append never writes (a key's has its sign,
+ * and fp4_kv_read's values have it in both).
  *   q     : device bf16 [total_q, q_heads, head_dim]; strides (elements) as in fp4_kv_append;
  *           16-byte aligned, strides multiples of 16 bytes.  dtype must be FP4_BF16.
  *   cu_q  : device int32 [seqs + 1], ascending from 0: queries cu_q[b] .. cu_q[b + 1] - 1 belong to

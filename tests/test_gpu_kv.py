@@ -632,3 +632,23 @@ def test_units_cut_in_two_schedules(cuda, group):
 def test_many_heads(cuda, queries):
     c = Cache([150, 20, 0], 40, 64, 16, fp4.NVFP4, seed=6)
     run_and_check(c, [queries] * 3, 1, strided=True)
+
+
+@pytest.mark.parametrize("queries", [1, 40])
+def test_value_scale_bytes_with_a_sign(cuda, queries):
+    """fp4_kv_append writes no scale byte with its sign bit set: attention counts one of a value block as
+    zero, one of a key block has its sign."""
+    c = Cache([40], 1, 64, 16, fp4.NVFP4)
+    q = torch.randn(queries, 4, 64, device=cuda).to(torch.bfloat16)
+    at = int(c.table_np[0, 1]), 0, 3, 0
+
+    def run(which, change):
+        arrays = [a.clone() for a in c.arrays]
+        change(arrays[which], arrays[which - 1])
+        return fp4.fp4_kv_attention(q, arrays, c.table, c.lens_t, max_q=queries, **c.scales)[0]
+
+    sign = lambda s, _: s.__setitem__(at, s[at] | 0x80)               # noqa: E731
+    zero = lambda s, _: s.__setitem__(at, 0)                          # noqa: E731
+    flip = lambda _, n: n[at[:3]][:8].bitwise_xor_(0x88)              # noqa: E731
+    assert torch.equal(run(3, sign), run(3, zero))
+    assert torch.equal(run(1, sign), run(1, flip))
