@@ -373,8 +373,8 @@ def fp4_kv_append(k: torch.Tensor, v: torch.Tensor, cache, slots: torch.Tensor, 
                   four_six: bool = False, k_global: torch.Tensor | None = None, v_global: torch.Tensor | None = None,
                   stream=None) -> None:
     """Quantise the keys and values of new tokens into the paged cache (from fp4_kv_alloc).
-    k, v: bf16 or fp32 [tokens, heads, head_dim], any token and head strides (slices of a fused
-    projection); slots: int64 [tokens], page * page_size + offset, negative to skip a row; k_global,
+    k, v: bf16 or fp32 [tokens, heads, head_dim], starting and strided (tokens, heads) on 32-byte
+    boundaries, as slices of a fused projection do; slots: int64 [tokens], page * page_size + offset, negative to skip a row; k_global,
     v_global: the fixed NVFP4 scales, amax / (6 * 448), or amax / (6 * 256) with four_six."""
     _check((_kv or _kv_native()).kv_append(k, v, *cache, slots, fmt, 1 if four_six else 0, k_global, v_global, _kv_stream(stream)))
 
@@ -402,11 +402,12 @@ def fp4_kv_attention(q: torch.Tensor, cache, table: torch.Tensor, lens: torch.Te
                      causal: bool = True, window: int = 0, want_lse: bool = False,
                      k_global: torch.Tensor | None = None, v_global: torch.Tensor | None = None,
                      out: torch.Tensor | None = None, stream=None, workspace: torch.Tensor | None = None):
-    """Attention of bf16 queries q [total_q, q_heads, head_dim] (any token and head strides) over the
-    cache.  Query head h reads key/value head h // (q_heads // heads); the queries of a sequence are
+    """Attention of bf16 queries q [total_q, q_heads, head_dim] (starting and strided on 16-byte boundaries)
+    over the cache.  Query head h reads key/value head h // (q_heads // heads); the queries of a sequence are
     its last tokens.  lens: int32 [seqs], keys of each sequence; cu_q: int32 [seqs + 1], queries
     cu_q[b]..cu_q[b+1]-1 belong to sequence b, at most max_q each (queries past max_q are not computed;
-    without cu_q every sequence has max_q, 1 by default); scale: 1 / sqrt(head_dim) by default; window: keys a query sees, itself the last one (0:
+    without cu_q every sequence has max_q, 1 by default; it chooses the kernel for the whole call, so a
+    prompt's chunk and single tokens are faster as two calls); scale: 1 / sqrt(head_dim) by default; window: keys a query sees, itself the last one (0:
     all).  Returns (out bf16 [total_q, q_heads, head_dim], lse float32 [total_q, q_heads] or None);
     a query that sees no key gives zeros and lse = -inf; rows of no sequence (from cu_q[-1] on) keep what
     `out` held, unset in a new one.  Rows of a pipeline wait that gave up are NaN (and named in the status

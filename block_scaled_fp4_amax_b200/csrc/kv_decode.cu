@@ -4,7 +4,8 @@
 // The cache is read once, so the work is bound by its bytes (144 a token and head at head_dim 128)
 // as long as unpacking keeps up: 1.5 instructions a value.  A unit of work is one (sequence, head).
 // All units' tiles of 128 tokens are laid end to end, and CTA i of n takes tiles [i T / n, (i + 1) T / n),
-// whatever the lengths (which only the device knows), so every CTA has the same number of tiles; a
+// whatever the lengths (which only the device knows), so every CTA has the same number of tiles (past
+// 256 sequences: those of a group of as many, which has its share of the CTAs whatever its lengths); a
 // unit that falls into several CTAs is written as fp32 partial results that a second, small launch
 // joins (launched programmatically: it is resident when the first one drains).
 //
@@ -17,7 +18,8 @@
 //   O^T += V^T P: 16 channels x 8 rows.  Thread g takes the channels [g D/8, (g + 1) D/8) of four
 //     tokens; the order of tokens is the one P's fragments have after an 8x8 transpose.
 // Values v * d (E2M1 times block scale) are exact in fp16; the per-tensor scales act on the fp32 sums.
-// Queries are scaled per row by a power of two so that fp16 holds their bf16 values exactly.  Weights
+// Queries are scaled per row by a power of two so that fp16 holds their bf16 values exactly (but for those
+// below 2^-31 of the row's largest: kv_query_scale).  Weights
 // exp2(z - m + 7) are rounded to fp16 for the product (m is the running maximum; it is raised only
 // when a score passes it by 8, so weights stay below 2^15, and those of 2^-21 of a row's largest keep
 // full precision) and summed unrounded.
@@ -598,7 +600,8 @@ cudaError_t decode_t(DecodeParams& p, cudaStream_t s) {
   // Short tables: a unit's few tiles one after another cost less than the joining launch where units fill the
   // SMs (512 units of 300, 1024 and 2048 tokens: 25, 33 and 40 us cut, 17, 29 and 43 us whole; 64
   // units of 1024: 12 and 16 us); up to three tiles they cost as much, and a launch less (8 units of
-  // 300: 7.7 us either way).
+  // 300: 7.7 us either way).  The host knows the table's width alone: short sequences in a wide table are
+  // cut (512 units of 150 to 300 tokens: 15.3 us in a table of 300, 22.5 us in one of 8192).
   const int span = p.a.max_pages << p.a.c.page_shift;
   p.whole = span <= 3 * kTile || (span <= 8 * kTile && (long long)p.a.seqs * p.a.c.heads >= 2 * num_sms());
   p.by_unit = (long long)p.a.seqs * p.a.c.heads <= n * chunks;

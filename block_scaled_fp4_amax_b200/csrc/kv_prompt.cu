@@ -17,7 +17,8 @@
 // over 6001 tokens: 92 us with one tile, 72 us so).  Tensor memory holds two
 // score tiles (128 columns each) and two output tiles (head_dim columns each).
 //
-// Numerics are those of kv_decode.cu: v * d and the power-of-two scaled queries are exact in fp16, the
+// Numerics are those of kv_decode.cu: v * d and the power-of-two scaled queries are exact in fp16 (queries
+// below 2^-31 of their row's largest aside), the
 // running maximum is raised only past 2^8 (the output tile is then rescaled in place, by the softmax
 // warps: the commit that announces the next scores also covers the product before it), weights
 // exp2(z - m + 7) rounded to fp16 for the product and summed unrounded.
@@ -666,7 +667,7 @@ cudaError_t launch_kv_prompt(const KvAttentionLaunch& L, cudaStream_t s) {
   p.qtiles = (int)(((long long)L.max_q * p.group + kRows - 1) / kRows);
   // Few units: the keys of each are split over the SMs that would be idle, four steps of 128 at least (48
   // queries over 60000 tokens, 32/8 heads: 829 us in 8 CTAs, 81 us in 144; 64 over 8192, 64/8 heads: 127
-  // and 42 us).
+  // and 42 us).  max_q rows of every sequence count, and the table's width.
   const long long units = kv_prompt_units(L);
   const long long steps = (((long long)L.max_pages << L.c.page_shift) + kKeys - 1) / kKeys;
   p.splits = 1;

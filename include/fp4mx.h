@@ -344,7 +344,9 @@ FP4_API fp4_status nvfp4_quantize_noalloc(const void* x, fp4_dtype dtype, long r
  *            for a padded row) writes nothing.  Slots of one call must differ: a slot named twice
  *            holds a mix of the two tokens' bytes.
  *   mode   : FP4_NV_PLAIN, or FP4_NV_FOUR_SIX (FP4_NVFP4 only).  Round to nearest.
- * A block holding Inf or NaN is left unspecified, as by the quantisers. */
+ * A block holding Inf or NaN is left unspecified, as by the quantisers.  Magnitudes beyond what the
+ * scales reach (6 * 448 * s_g under FP4_NVFP4) saturate, as there, but are not counted: the call has
+ * no fp4_counts. */
 FP4_API fp4_status fp4_kv_append(const void* k, const void* v, fp4_dtype dtype, long tokens, long k_stride,
                                  long k_head_stride, long v_stride, long v_head_stride, const long long* slots,
                                  fp4_format format, int block, int mode, const float* k_global,
@@ -374,9 +376,10 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  *   iff j < lens[b], and j <= its position (causal != 0), and j > its position - window (window > 0),
  *   and the key has a page.  A query that sees no key gives zeros and lse = -inf.
  * Scores, softmax statistics and sums are fp32; keys and values enter the products exactly, the
- * queries too (scaled per row by a power of two), and the softmax weights, fp32 in the sum that
- * divides, are rounded to fp16 for the product with V: off by 2^-11 of a weight, or by 2^-32 of the
- * row's largest weight where that is more.  A query row holding
+ * queries (scaled per row by a power of two) too, but for values below 2^-31 of their row's largest,
+ * which are off by 2^-39 of it at most; and the softmax weights, fp32 in the sum that divides, are
+ * rounded to fp16 for the product with V: off by 2^-11 of a weight, or by 2^-32 of the row's largest
+ * weight where that is more.  A query row holding
  * Inf or NaN is unspecified; an MXFP4 scale byte outside 104 .. 140 counts as the nearest of these;
  * an E4M3 NaN scale byte of a key gives NaN in the rows that see it, one of a value block counts as 0
  * (a product with a weight of 0 would carry it into rows that do not see the token), and so does a
@@ -387,15 +390,18 @@ FP4_API fp4_status fp4_kv_read(const unsigned char* kq, const unsigned char* ks,
  *   cu_q  : device int32 [seqs + 1], ascending from 0: queries cu_q[b] .. cu_q[b + 1] - 1 belong to
  *           sequence b; NULL: max_q for every sequence (total_q == seqs * max_q).  Rows from
  *           cu_q[seqs] on are left as they were.
- *   max_q : at least the largest number of queries of a sequence; further ones are not computed.
+ *   max_q : at least the largest number of queries of a sequence; further ones are not computed.  It
+ *           chooses the kernel for the whole call: up to 32 rows (max_q * q_heads / heads) one that
+ *           splits long sequences over the device, beyond it one that takes 256 rows a block.  Where
+ *           a prompt's chunk goes beside single tokens, two calls, one for each, are faster.
  *   lens  : device int32 [seqs]: keys of each sequence, the new tokens' included (append first);
  *           negative counts as 0, more than max_pages * page_size as that.
  *   out   : device bf16 [total_q, q_heads, head_dim], 16-byte aligned.
  *   Limits: total_q <= 2^24, seqs <= 32768, max_pages * page_size <= 2^30, q_heads <= 4096.
  *   lse   : device float [total_q, q_heads] or NULL: natural log of the sum of exp(scale q k).
  *   workspace : device, 16-byte aligned, >= fp4_workspace_size(FP4_OP_KV_ATTENTION, total_q, q_heads)
- *           bytes (asked with the call's device current); clobbered, needs no initialisation.  Calls that overlap need one each.  Its first 4
- *           bytes are a status word, 0 when every pipeline wait of the call ended; otherwise bit i
+ *           bytes (asked with the call's device current); clobbered, needs no initialisation.  Calls
+ *           that overlap need one each.  Its first 4 bytes are a status word, 0 when every pipeline wait of the call ended; otherwise bit i
  *           names the wait that gave up (many rows only: 0 scores, 1 the output, 2 and 3 a free key
  *           and value stage, 4 the queries, 5 and 6 a full key and value stage, 7 weights), and the
  *           rows of out and lse whose work was cut short are NaN, so that a caller who cannot read

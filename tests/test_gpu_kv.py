@@ -652,3 +652,13 @@ def test_value_scale_bytes_with_a_sign(cuda, queries):
     flip = lambda _, n: n[at[:3]][:8].bitwise_xor_(0x88)              # noqa: E731
     assert torch.equal(run(3, sign), run(3, zero))
     assert torch.equal(run(1, sign), run(1, flip))
+
+
+@pytest.mark.parametrize("queries", [1, 48])
+def test_queries_near_the_smallest_numbers(cuda, queries):
+    """Rows that no power of two of fp32 brings to fp16's upper end, subnormals among them: exact all the same."""
+    c = Cache([200], 1, 64, 16, fp4.NVFP4, seed=8)
+    q = (torch.randn(queries, 4, 64, generator=torch.Generator().manual_seed(2)) * 2.0 ** -124).to(torch.bfloat16)
+    out, lse = fp4.fp4_kv_attention(q.to(cuda), c.arrays, c.table, c.lens_t, max_q=queries, scale=2.0 ** 122, want_lse=True, **c.scales)
+    ref = attention64(q.double().numpy(), c.k64[0], c.v64[0], 2.0 ** 122, True, 0)
+    check(out, lse, ref, 200, 64, np.abs(c.v64[0]).max())
