@@ -69,12 +69,17 @@ __device__ __forceinline__ uint32_t kv_value_scales(uint32_t b0, uint32_t b1) {
 // Power of two that brings a row of bf16 queries (largest magnitude `m`, an fp32 bit pattern) to a
 // maximum in [2^14, 2^15): fp16 then holds every value down to 2^-31 of the largest exactly, and
 // smaller ones to 2^-39 of it.  (The power is at most 2^127.  Rows below 2^-113, which it leaves smaller,
-// hold multiples of 2^-133: 2^-6 then, so they are exact.)  `down` is its reciprocal.
+// hold multiples of 2^-133: 2^-6 then, so they are exact.  A row of zeros takes 2^64, so that any scale
+// times `down` is a number.)  `down` is its reciprocal.
 __device__ __forceinline__ void kv_query_scale(uint32_t m, float& up, float& down) {
-  const uint32_t f = m == 0u ? 127u : min(268u - (m >> 23), 254u);
+  const uint32_t f = m == 0u ? 191u : min(268u - (m >> 23), 254u);
   up = __uint_as_float(f << 23);
   down = f < 254u ? __uint_as_float((254u - f) << 23) : __uint_as_float(0x00400000u);
 }
+
+// Score in log2 units = sum * coefficient.  The call's scale meets the row's power of two first: they make
+// up for each other where queries are very large or small, and the product with `g` stays normal.
+__device__ __forceinline__ float kv_coefficient(float scale, float down, float g) { return scale * down * 1.44269504f * g; }
 
 // 1 / sum of weights (0 for a row that saw no key, NaN for a NaN sum), and the row's log-sum-exp.
 // Weights are exp2(z + bias), bias = kShift - maximum.

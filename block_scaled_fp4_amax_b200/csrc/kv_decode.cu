@@ -222,7 +222,7 @@ __global__ void __launch_bounds__(32 * kWarps, DecodeCfg<NT>::kCtas) kv_decode_k
       m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, 2));
       float up, down;
       kv_query_scale(m, up, down);
-      float c = a.scale * 1.44269504f * gk * down;
+      float c = kv_coefficient(a.scale, down, gk);
       kv_positive(c, up);
       coef[k] = c;
 #pragma unroll

@@ -201,7 +201,7 @@ __device__ __forceinline__ void run_unit(const PromptParams& p, const KvSpan& sp
         for (int i = 0; i < D / 2; ++i) top = max(top, max((raw[i] & 0x7FFFu) << 16, raw[i] & 0x7FFF0000u));
         float up, down;
         kv_query_scale(top, up, down);
-        coef = a.scale * 1.44269504f * (NV ? __ldg(a.c.k_global) : 1.0f) * down;
+        coef = kv_coefficient(a.scale, down, NV ? __ldg(a.c.k_global) : 1.0f);
         kv_positive(coef, up);
         const uint32_t q_tile = smem + L::kQ + m * L::kTile;
 #pragma unroll

@@ -662,3 +662,15 @@ def test_queries_near_the_smallest_numbers(cuda, queries):
     out, lse = fp4.fp4_kv_attention(q.to(cuda), c.arrays, c.table, c.lens_t, max_q=queries, scale=2.0 ** 122, want_lse=True, **c.scales)
     ref = attention64(q.double().numpy(), c.k64[0], c.v64[0], 2.0 ** 122, True, 0)
     check(out, lse, ref, 200, 64, np.abs(c.v64[0]).max())
+
+
+@pytest.mark.parametrize("queries", [1, 48])
+@pytest.mark.parametrize("size,scale", [(2.0 ** 120, 2.0 ** -122), (2.0 ** -126, 1.75 * 2.0 ** 127)])
+def test_scales_of_very_large_and_small_queries(cuda, queries, size, scale):
+    """Scales whose product with the base's logarithm or the keys' scale alone leaves fp32's normal numbers."""
+    c = Cache([200], 1, 64, 16, fp4.NVFP4, seed=8)
+    q = (torch.randn(queries, 4, 64, generator=torch.Generator().manual_seed(2)) * size).to(torch.bfloat16)
+    q[queries // 2, 1] = 0
+    out, lse = fp4.fp4_kv_attention(q.to(cuda), c.arrays, c.table, c.lens_t, max_q=queries, scale=scale, want_lse=True, **c.scales)
+    ref = attention64(q.double().numpy(), c.k64[0], c.v64[0], scale, True, 0)
+    check(out, lse, ref, 200, 64, np.abs(c.v64[0]).max())
