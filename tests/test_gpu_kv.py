@@ -674,3 +674,20 @@ def test_scales_of_very_large_and_small_queries(cuda, queries, size, scale):
     out, lse = fp4.fp4_kv_attention(q.to(cuda), c.arrays, c.table, c.lens_t, max_q=queries, scale=scale, want_lse=True, **c.scales)
     ref = attention64(q.double().numpy(), c.k64[0], c.v64[0], scale, True, 0)
     check(out, lse, ref, 200, 64, np.abs(c.v64[0]).max())
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_append_mx_maxima_at_powers_of_two(cuda, dtype):
+    """Block maxima that are powers of two, and the numbers next to them: the oracle's bytes."""
+    rng = np.random.default_rng(5)
+    exps = np.arange(-20, 14)
+    x = rng.uniform(-0.9, 0.9, (len(exps), 3, 64)).astype(np.float32)
+    step = np.float32(torch.finfo(dtype).eps)
+    x[:, 0, ::32], x[:, 1, ::32], x[:, 2, ::32] = 1, 1 - step / 2, -1 - step
+    t = torch.from_numpy(np.ldexp(x, exps[:, None, None]).astype(np.float32)).to(dtype)
+    assert torch.equal(t[:, :, 0].double(), torch.from_numpy(np.ldexp(x[:, :, 0].astype(np.float64), exps[:, None])))
+    cache = fp4.fp4_kv_alloc(3, 3, 16, 64, fp4.MXFP4, device=cuda)
+    fp4.fp4_kv_append(t.to(cuda), t.to(cuda), cache, torch.arange(len(exps), device=cuda), fp4.MXFP4)
+    q, s = quantise(t.float().numpy(), fp4.MXFP4, 1.0)
+    for got, want in zip(cache, (q, s, q, s)):
+        assert np.array_equal(got.transpose(1, 2).reshape(48, 3, -1)[:len(exps)].cpu().numpy(), want)
